@@ -237,7 +237,7 @@ def _diff(s):
         lh.diff_attn_fwd(cfg, s["q"], s["k"], s["v"], s["lam"], s["o"], s["ws"], cu=s["cu"])
         if not c["train"]:
             return {"o": s["o"]}
-        lh.diff_attn_bwd(cfg, s["do"], s["q"], s["k"], s["v"], s["lam"], s["o"], s["ws"], s["dq"], s["dk"], s["dv"], s["dlam"], cu=s["cu"])
+        lh.diff_attn_bwd(cfg, s["do"], s["q"], s["k"], s["v"], s["lam"], s["ws"], s["dq"], s["dk"], s["dv"], s["dlam"], cu=s["cu"])
         return {"o": s["o"], "dq": s["dq"], "dk": s["dk"], "dv": s["dv"], "dlam": s["dlam"]}
     B, N, H, Hk, D = c["B"], c["N"], c["H"], c["Hk"], c["D"]
     G, h = H // Hk, D // 2
