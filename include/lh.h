@@ -384,6 +384,127 @@ lh_status lh_cp_attn_bwd(const lh_config* cfg, int world, int rank, const int32_
 lh_status lh_cp_spread(const lh_config* cfg, int world, int rank, const float* dqs, const float* dks,
                        const float* dvs, const int32_t* slot_loc, void* dq, void* dk, void* dv, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the layer around the attention: layer norm, rotary positions,
+ * differential attention. They take the token layouts above, with row strides
+ * where a caller keeps several tensors in one buffer (a fused projection's
+ * output, a chunk of a longer sequence). They allocate nothing and keep
+ * nothing between calls: two calls may run at the same time as long as each
+ * has its own outputs and its own workspace (that holds for the replays of two
+ * captured graphs too). Inputs and outputs do not overlap, except where an
+ * entry point says so.
+ * ------------------------------------------------------------------------- */
+
+/* Layer norm of M rows of d values:
+ *   z = (x - mean) rstd, rstd = 1 / sqrt(var + eps),  y = z w + b.
+ * Sums in fp32 (the variance from the centred values), one rounding into
+ * dtype. M = 0 launches nothing (lh_norm_bwd then writes zeros to dw, db). */
+#define LH_NORM_MAX_D 16384
+typedef struct {
+  long long M;          /* rows, 0 .. 2^40 */
+  int d;                /* values per row, 1 .. LH_NORM_MAX_D */
+  lh_dtype dtype;       /* x, y, dy, dx */
+  lh_dtype wdtype;      /* w, b, dw, db */
+  long long ldx, ldy;   /* elements between rows of x and dx, and of y and dy (0: d; else >= d) */
+  float eps;            /* >= 0, finite */
+} lh_norm_config;
+
+/* Bytes of lh_norm_bwd's workspace (0 for M = 0). Pure host function.
+ * Errors of all three: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_ALIGN,
+ * LH_ERR_WORKSPACE, LH_ERR_CUDA. */
+lh_status lh_norm_plan(const lh_norm_config* cfg, size_t* ws_bytes);
+
+/* y from x [M][d], w and b [d] (either may be NULL: 1 and 0). mean and rstd
+ * [M] float may be NULL where no backward pass follows. y may be x itself
+ * (same stride). */
+lh_status lh_norm_fwd(const lh_norm_config* cfg, const void* x, const void* w, const void* b, void* y, float* mean,
+                      float* rstd, void* stream);
+
+/* With g = dy w: dx = rstd (g - mean(g) - z mean(g z)), dw = sum over rows of
+ * dy z, db = sum over rows of dy (either may be NULL). mean and rstd as
+ * lh_norm_fwd left them. dw and db are added in a fixed order: the same bits
+ * in every run. ws: lh_norm_plan's bytes, contents not kept. dx may be dy
+ * itself (where ldx = ldy). */
+lh_status lh_norm_bwd(const lh_norm_config* cfg, const void* dy, const void* x, const void* w, const float* mean,
+                      const float* rstd, void* dx, void* dw, void* db, void* ws, size_t ws_bytes, void* stream);
+
+/* Rotary positions. Pair i of a row turns by pos[axis[i]] * freq[i] (radians):
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * the elements behind the first `rot` are copied. Angles in 64 bits, rotation
+ * in fp32, one rounding into dtype. */
+#define LH_ROPE_MAX_AXES 8
+#define LH_ROPE_MAX_D 1024
+typedef enum {
+  LH_ROPE_HALF = 0,    /* pair i: elements i and i + rot/2 */
+  LH_ROPE_NEXT = 1     /* pair i: elements 2i and 2i + 1 */
+} lh_rope_pairs;
+typedef struct {
+  int B, N;             /* sequences (>= 0) and tokens of each (>= 0); B * N < 2^32 */
+  int H, Hk, D;         /* heads of q (>= 1) and k (>= 0), elements per row, 2 .. LH_ROPE_MAX_D */
+  int rot;              /* rotated elements, even, 2 .. D */
+  int axes;             /* position axes, 1 .. LH_ROPE_MAX_AXES */
+  lh_dtype dtype;
+  lh_rope_pairs pairs;
+  int pos64;            /* positions are int64 (else int32) */
+  /* elements between tokens (ld) and between sequences (bs) of q, k and the
+   * outputs; 0: contiguous [B][N][heads][D]. ld >= heads * D. */
+  long long q_ld, q_bs, k_ld, k_bs, qo_ld, qo_bs, ko_ld, ko_bs;
+  /* positions: pos[a * pos_as + b * pos_bs + t]; pos_bs = 0: the sequences share them */
+  long long pos_as, pos_bs;
+} lh_rope_config;
+
+/* qo, ko = rotated q, k (q and k themselves for rotation in place, with the
+ * same strides). inverse != 0 turns the other way: the backward pass, with
+ * dq, dk of the outputs as q, k. freq [rot/2] double and axis [rot/2] int32 are
+ * device tables that the caller keeps; an axis outside [0, axes) is reported
+ * by lh_get_device_error (LH_ERR_DEVICE, detail 401) and read as 0. k and ko
+ * may be NULL when Hk = 0. */
+lh_status lh_rope(const lh_rope_config* cfg, const void* q, const void* k, const void* pos, const double* freq,
+                  const int32_t* axis, int inverse, void* qo, void* ko, void* stream);
+
+/* Causal differential attention: a head's q and k rows of D elements hold two
+ * maps of D/2 (first half: map 1, second half: map 2),
+ *   o = A1 v - lam A2 v,  A_m = softmax(q_m k_m^T / sqrt(D/2) + causal mask).
+ * Query head h reads key/value head h / (H / Hk). */
+typedef struct {
+  int B;                     /* sequences, >= 1 */
+  int T;                     /* token rows of q, k, v, o in all, >= 0, < 2^30 */
+  int H, Hk, D;              /* query heads, key/value heads (Hk divides H), D in {64, 128} */
+  lh_dtype dtype;            /* q, k, v, lam, o and the gradients */
+  int packed;                /* 0: B sequences of T / B rows each (B divides T); 1: `cu` gives them */
+  int train;                 /* keep what lh_diff_attn_bwd needs */
+  long long ldq, ldk, ldv, ldo;  /* elements between token rows of q (and dq), k (and dk), v (and dv),
+                                    o (and dout); 0: contiguous; multiples of 8, >= heads * D */
+} lh_diff_config;
+
+typedef struct {
+  size_t saved_bytes;        /* written by lh_diff_attn_fwd, read by lh_diff_attn_bwd */
+  size_t ws_bytes;           /* scratch of lh_diff_attn_bwd (0 unless train) */
+} lh_diff_plan_t;
+
+/* Sizes. Pure host function. Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE,
+ * LH_ERR_MODE (packed, train not 0 / 1). */
+lh_status lh_diff_plan(const lh_diff_config* cfg, lh_diff_plan_t* out);
+
+/* q [T][H][D], k, v [T][Hk][D], lam [H] (device, dtype) -> o [T][H][D].
+ * packed: cu [B + 1] int32 (device), sequence b in rows cu[b] .. cu[b+1]-1,
+ * non-decreasing, within [0, T] (anything else is reported by
+ * lh_get_device_error, LH_ERR_DEVICE, detail 402, with no access out of
+ * bounds); sequences may be empty; rows outside [cu[0], cu[B]) are neither
+ * read nor written, and a sequence's rows are read for that sequence alone.
+ * packed = 0: cu is NULL. bf16 I/O runs on the tensor cores (fp16 operands
+ * with a power of two per sequence and head, as in lh_attn_fwd; a non-finite
+ * value is reported, LH_ERR_DEVICE detail 102), fp32 in fp32 arithmetic. */
+lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void* k, const void* v, const void* lam,
+                           const int32_t* cu, void* o, void* saved, size_t saved_bytes, void* stream);
+
+/* Gradients of lh_diff_attn_fwd (cfg->train = 1, same cfg, inputs and
+ * saved): dq, dk, dv (rows outside the sequences are not written) and
+ * dlam [H]. Deterministic, shared heads included (no atomics). */
+lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const void* q, const void* k, const void* v,
+                           const void* lam, const int32_t* cu, const void* saved, size_t saved_bytes,
+                           void* ws, size_t ws_bytes, void* dq, void* dk, void* dv, void* dlam, void* stream);
+
 /* Reads and clears the device error word set by bounded waits and device
  * checks (LH_OK, LH_ERR_TIMEOUT or LH_ERR_DEVICE); *detail receives the
  * kernel-specific code (0 if none). Synchronises `stream`. */

@@ -1,0 +1,462 @@
+// Layer norm of the rows of a matrix, forward and backward, with the reduction
+// of the weight's and the bias's gradient.
+//
+//   z = (x - mean) rstd,  y = z w + b,        rstd = 1 / sqrt(var + eps)
+//   g = dy w,  dx = rstd (g - mean(g) - z mean(g z)),
+//   dw = sum over rows of dy z,  db = sum over rows of dy
+//
+// Everything is summed in fp32 and rounded once on the way out; the variance is
+// formed from the centred values (a second pass over the registers, not over
+// memory), so a row whose mean is far above its deviation keeps its digits.
+//
+// Bound by HBM: x is read and y written once; the backward reads x and dy and
+// writes dx once. A row is held in registers by a group of threads, 8 values
+// each: G = 4 .. 32 lanes of a warp for rows of up to 256 values (several rows
+// to a warp, sums by shuffles alone), a whole block for longer rows (one
+// barrier per reduction, the partial sums alternating between two buffers).
+// Blocks stay resident and walk the rows with a stride, R rows at a time, so
+// that the weights are loaded once and R rows' loads are in flight together;
+// the backward keeps its columns' dw and db in registers (in shared memory for
+// rows of more than 8,192 values, where 512 threads hold 32 columns each and
+// the registers do not suffice) and writes one partial row per block, which a
+// second kernel adds in a fixed order: no atomics, the same bits every run.
+//
+// Rows of odd length, or whose stride is no multiple of 8 elements, are read
+// element by element with the columns dealt out to neighbouring lanes (VEC =
+// false), which keeps the accesses of a warp contiguous.
+#include "lh_common.cuh"
+
+namespace lh {
+namespace {
+
+constexpr int kNormThreads = 512;      // threads that hold one long row at most
+
+struct NormArgs {
+  const void *x, *w, *b, *dy;
+  void *y, *dx;
+  float *mean, *rstd, *part;
+  long long M, ldx, ldy;
+  int d, wbf16;
+  float eps, inv_d;
+};
+
+template <typename T> __device__ __forceinline__ float ld_f32(const T* p);
+template <> __device__ __forceinline__ float ld_f32<float>(const float* p) { return __ldg(p); }
+template <> __device__ __forceinline__ float ld_f32<__nv_bfloat16>(const __nv_bfloat16* p) {
+  return __bfloat162float(*p);
+}
+__device__ __forceinline__ void st_f32(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// The 8 columns that thread t of a group of `gs` holds in its vector v:
+// neighbours (VEC), or one of every gs. Columns past d read as 0.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int v, int i, int t, int gs) {
+  return VEC ? (v * gs + t) * 8 + i : (v * 8 + i) * gs + t;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_cols(const T* row, int v, int t, int gs, int d, float (&x)[8]) {
+  if (VEC) {
+    const int c = (v * gs + t) * 8;
+    if (c < d) {
+      Vec8<T>::load_f32(row + c, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = col_of<false>(v, i, t, gs);
+      x[i] = c < d ? ld_f32(row + c) : 0.f;
+    }
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_cols(T* row, int v, int t, int gs, int d, const float (&x)[8]) {
+  if (VEC) {
+    const int c = (v * gs + t) * 8;
+    if (c < d) Vec8<T>::store_f32(row + c, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = col_of<false>(v, i, t, gs);
+      if (c < d) st_f32(row + c, x[i]);
+    }
+  }
+}
+// weight or bias columns (NULL: the given constant)
+template <bool VEC>
+__device__ __forceinline__ void load_w(const void* w, int bf16, float none, int v, int t, int gs, int d,
+                                       float (&x)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = none;
+  } else if (bf16) {
+    load_cols<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), v, t, gs, d, x);
+  } else {
+    load_cols<float, VEC>(static_cast<const float*>(w), v, t, gs, d, x);
+  }
+}
+
+// Sum of each of n values over the threads of a row's group. G > 0: lanes of a
+// warp. G = 0: the block, through red (32 * n floats; the caller alternates
+// between two of them, so one barrier per reduction suffices: a buffer is
+// written again only after the other one's barrier).
+template <int G, int n>
+__device__ __forceinline__ void group_sum(float (&v)[n], float* red) {
+#pragma unroll
+  for (int o = (G ? G : 32) / 2; o; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  }
+  if (G == 0) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < n; ++k) red[warp * n + k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] = lane < nw ? red[lane * n + k] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+      for (int k = 0; k < n; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+  }
+}
+
+template <typename T, bool VEC, int G, int NV, int R>
+__global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormArgs a) {
+  __shared__ float red[G ? 1 : 2 * 32 * R];
+  const int gs = G ? G : (int)blockDim.x, t = G ? (int)threadIdx.x % G : (int)threadIdx.x;
+  const int groups = G ? (int)blockDim.x / G : 1, grp = G ? (int)threadIdx.x / G : 0;
+  const T* x = static_cast<const T*>(a.x);
+  T* y = static_cast<T*>(a.y);
+  float w[NV][8], b[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[v]);
+    load_w<VEC>(a.b, a.wbf16, 0.f, v, t, gs, a.d, b[v]);
+  }
+  // the block's rows: `base` is the same for the whole block, so every thread
+  // takes part in every reduction
+  const long long step = (long long)gridDim.x * groups;
+  for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R) {
+    float xv[R][NV][8], s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long m = base + r * step + grp;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) load_cols<T, VEC>(x + (m < a.M ? m : 0) * a.ldx, v, t, gs, m < a.M ? a.d : 0, xv[r][v]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[r] += xv[r][v][i];
+    }
+    group_sum<G, R>(s, red);
+    float mu[R], q[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mu[r] = s[r] * a.inv_d;
+      q[r] = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c = col_of<VEC>(v, i, t, gs) < a.d ? xv[r][v][i] - mu[r] : 0.f;
+          xv[r][v][i] = c;
+          q[r] = fmaf(c, c, q[r]);
+        }
+    }
+    group_sum<G, R>(q, red + (G ? 0 : 32 * R));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long m = base + r * step + grp;
+      const float rs = 1.f / sqrtf(q[r] * a.inv_d + a.eps);
+      if (m < a.M) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = fmaf(xv[r][v][i] * rs, w[v][i], b[v][i]);
+          store_cols<T, VEC>(y + m * a.ldy, v, t, gs, a.d, o);
+        }
+        if (t == 0) {
+          if (a.mean) a.mean[m] = mu[r];
+          if (a.rstd) a.rstd[m] = rs;
+        }
+      }
+    }
+  }
+}
+
+// ACC: dw and db of this thread's columns in registers (false: in shared memory).
+template <typename T, bool VEC, int G, int NV, int R, bool ACC>
+__global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormArgs a) {
+  extern __shared__ float dyn[];
+  __shared__ float red[G ? 1 : 2 * 32 * 2 * R];
+  const int gs = G ? G : (int)blockDim.x, t = G ? (int)threadIdx.x % G : (int)threadIdx.x;
+  const int groups = G ? (int)blockDim.x / G : 1, grp = G ? (int)threadIdx.x / G : 0;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  T* dx = static_cast<T*>(a.dx);
+  float dw[ACC ? NV : 1][8], db[ACC ? NV : 1][8];
+  if (ACC) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[ACC ? v : 0][i] = db[ACC ? v : 0][i] = 0.f;
+  } else {
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) dyn[c] = 0.f;
+    __syncthreads();
+  }
+  const long long step = (long long)gridDim.x * groups;
+  int flip = 0;
+  for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R, flip ^= 1) {
+    float xv[R][NV][8], gv[R][NV][8], mu[R], rs[R], s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long m = base + r * step + grp, mm = m < a.M ? m : 0;
+      const int d = m < a.M ? a.d : 0;
+      mu[r] = m < a.M ? __ldg(a.mean + mm) : 0.f;
+      rs[r] = m < a.M ? __ldg(a.rstd + mm) : 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        load_cols<T, VEC>(x + mm * a.ldx, v, t, gs, d, xv[r][v]);
+        load_cols<T, VEC>(dy + mm * a.ldy, v, t, gs, d, gv[r][v]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2 * R; ++r) s[r] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float w[8];
+      load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool in = col_of<VEC>(v, i, t, gs) < a.d;
+          const float z = in ? (xv[r][v][i] - mu[r]) * rs[r] : 0.f, g = gv[r][v][i];
+          if (a.part) {
+            if (ACC) {
+              dw[ACC ? v : 0][i] = fmaf(g, z, dw[ACC ? v : 0][i]);
+              db[ACC ? v : 0][i] += g;
+            } else if (in) {
+              const int c = col_of<VEC>(v, i, t, gs);
+              dyn[c] = fmaf(g, z, dyn[c]);
+              dyn[a.d + c] += g;
+            }
+          }
+          const float gw = g * w[i];
+          xv[r][v][i] = z;
+          gv[r][v][i] = gw;
+          s[2 * r] += gw;
+          s[2 * r + 1] = fmaf(gw, z, s[2 * r + 1]);
+        }
+      }
+    }
+    group_sum<G, 2 * R>(s, red + (G ? 0 : flip * 64 * R));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long m = base + r * step + grp;
+      if (m < a.M) {
+        const float c1 = s[2 * r] * a.inv_d, c2 = s[2 * r + 1] * a.inv_d;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = rs[r] * ((gv[r][v][i] - c1) - xv[r][v][i] * c2);
+          store_cols<T, VEC>(dx + m * a.ldx, v, t, gs, a.d, o);
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + (size_t)blockIdx.x * 2 * a.d;
+  if (!ACC) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) out[c] = dyn[c];
+  } else if (G == 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = col_of<VEC>(v, i, t, gs);
+        if (c < a.d) {
+          out[c] = dw[ACC ? v : 0][i];
+          out[a.d + c] = db[ACC ? v : 0][i];
+        }
+      }
+  } else {
+    // the block's groups hold the same columns: add them in group order
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = col_of<VEC>(v, i, t, gs);
+        if (c < a.d) {
+          dyn[(2 * grp) * a.d + c] = dw[ACC ? v : 0][i];
+          dyn[(2 * grp + 1) * a.d + c] = db[ACC ? v : 0][i];
+        }
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) {
+      float s = 0.f;
+      for (int k = 0; k < groups; ++k) s += dyn[2 * k * a.d + c];
+      out[c] = s;
+    }
+  }
+}
+
+// dw and db: the blocks' partial rows added in block order, 32 columns to a
+// block, 32 strands that a fixed tree joins.
+__global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ part, int nb, int d, void* dw,
+                                                      void* db, int wbf16) {
+  __shared__ float sm[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  if (c < 2 * d) {
+    const float* p = part + c;
+    for (int k = threadIdx.y; k < nb; k += 32) s += __ldg(p + (size_t)k * 2 * d);
+  }
+  sm[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  float v = sm[threadIdx.x][threadIdx.y];      // column threadIdx.y, strand threadIdx.x
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int cc = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && cc < 2 * d) {
+    void* dst = cc < d ? dw : db;
+    const int k = cc < d ? cc : cc - d;
+    if (dst) {
+      if (wbf16) static_cast<__nv_bfloat16*>(dst)[k] = __float2bfloat16_rn(v);
+      else static_cast<float*>(dst)[k] = v;
+    }
+  }
+}
+
+// How a row of d values is dealt out: lanes of a warp up to 256 values, a block
+// beyond; nv vectors of 8 per thread.
+struct NormShape {
+  int G, threads, nv;
+};
+NormShape norm_shape(int d) {
+  const int nvec = (d + 7) / 8;
+  if (nvec <= 32) {
+    int G = 4;
+    while (G < nvec) G *= 2;
+    return {G, 256, 1};
+  }
+  const int nv = nvec <= kNormThreads ? 1 : nvec <= 2 * kNormThreads ? 2 : 4, th = (nvec + nv - 1) / nv;
+  return {0, (th + 31) / 32 * 32, nv};
+}
+constexpr int kNormSMs = 148;
+// Resident blocks: 1,024 threads to an SM (about 64 registers each).
+int norm_blocks(const NormShape& s, long long M, int R) {
+  const long long groups = s.G ? s.threads / s.G : 1, need = (M + groups * R - 1) / (groups * R);
+  const long long most = (long long)kNormSMs * (1024 / s.threads < 1 ? 1 : 1024 / s.threads);
+  return (int)(need < most ? need : most);
+}
+constexpr int kRF = 2, kRB = 2;      // rows in flight per group, forward and backward (nv = 1)
+
+template <typename T, bool VEC>
+cudaError_t fwd_t(const NormShape& s, const NormArgs& a, cudaStream_t st) {
+  const int nb = norm_blocks(s, a.M, s.nv == 1 ? kRF : 1);
+  switch (s.G) {
+    case 4: k_norm_fwd<T, VEC, 4, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
+    case 8: k_norm_fwd<T, VEC, 8, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
+    case 16: k_norm_fwd<T, VEC, 16, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
+    case 32: k_norm_fwd<T, VEC, 32, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
+    default:
+      if (s.nv == 1) k_norm_fwd<T, VEC, 0, 1, kRF><<<nb, s.threads, 0, st>>>(a);
+      else if (s.nv == 2) k_norm_fwd<T, VEC, 0, 2, 1><<<nb, s.threads, 0, st>>>(a);
+      else k_norm_fwd<T, VEC, 0, 4, 1><<<nb, s.threads, 0, st>>>(a);
+  }
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t bwd_t(const NormShape& s, const NormArgs& a, int nb, cudaStream_t st) {
+  const size_t sm = s.G ? (size_t)(s.threads / s.G) * 2 * a.d * 4 : s.nv == 4 ? (size_t)2 * a.d * 4 : 0;
+  switch (s.G) {
+    case 4: k_norm_bwd<T, VEC, 4, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
+    case 8: k_norm_bwd<T, VEC, 8, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
+    case 16: k_norm_bwd<T, VEC, 16, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
+    case 32: k_norm_bwd<T, VEC, 32, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
+    default:
+      if (s.nv == 1) {
+        k_norm_bwd<T, VEC, 0, 1, kRB, true><<<nb, s.threads, sm, st>>>(a);
+      } else if (s.nv == 2) {
+        k_norm_bwd<T, VEC, 0, 2, 1, true><<<nb, s.threads, sm, st>>>(a);
+      } else {
+        auto kern = k_norm_bwd<T, VEC, 0, 4, 1, false>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+        kern<<<nb, s.threads, sm, st>>>(a);
+      }
+  }
+  count_launch();
+  return cudaGetLastError();
+}
+
+bool norm_vec(const lh_norm_config& c, long long ldx, long long ldy) {
+  return c.d % 8 == 0 && ldx % 8 == 0 && ldy % 8 == 0;
+}
+
+}  // namespace
+
+// Partial rows of dw and db: one of 2 d floats per block of the backward kernel.
+size_t norm_ws_bytes(const lh_norm_config& c) {
+  const NormShape s = norm_shape(c.d);
+  return (size_t)norm_blocks(s, c.M, s.nv == 1 ? kRB : 1) * 2 * c.d * sizeof(float);
+}
+
+cudaError_t launch_norm_fwd(const lh_norm_config& c, const void* x, const void* w, const void* b, void* y,
+                            float* mean, float* rstd, cudaStream_t st) {
+  if (c.M == 0) return cudaSuccess;
+  NormArgs a{};
+  a.x = x; a.w = w; a.b = b; a.y = y; a.mean = mean; a.rstd = rstd;
+  a.M = c.M; a.ldx = c.ldx ? c.ldx : c.d; a.ldy = c.ldy ? c.ldy : c.d; a.d = c.d;
+  a.wbf16 = c.wdtype == LH_BF16; a.eps = c.eps; a.inv_d = 1.f / (float)c.d;
+  const NormShape s = norm_shape(c.d);
+  const bool vec = norm_vec(c, a.ldx, a.ldy);
+  if (c.dtype == LH_BF16)
+    return vec ? fwd_t<__nv_bfloat16, true>(s, a, st) : fwd_t<__nv_bfloat16, false>(s, a, st);
+  return vec ? fwd_t<float, true>(s, a, st) : fwd_t<float, false>(s, a, st);
+}
+
+cudaError_t launch_norm_bwd(const lh_norm_config& c, const void* dy, const void* x, const void* w, const float* mean,
+                            const float* rstd, void* dx, void* dw, void* db, float* part, cudaStream_t st) {
+  NormArgs a{};
+  a.x = x; a.w = w; a.dy = dy; a.dx = dx; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+  a.part = dw || db ? part : nullptr;
+  a.M = c.M; a.ldx = c.ldx ? c.ldx : c.d; a.ldy = c.ldy ? c.ldy : c.d; a.d = c.d;
+  a.wbf16 = c.wdtype == LH_BF16; a.eps = c.eps; a.inv_d = 1.f / (float)c.d;
+  const NormShape s = norm_shape(c.d);
+  const int nb = norm_blocks(s, c.M, s.nv == 1 ? kRB : 1);
+  if (c.M > 0) {
+    const bool vec = norm_vec(c, a.ldx, a.ldy);
+    cudaError_t e;
+    if (c.dtype == LH_BF16)
+      e = vec ? bwd_t<__nv_bfloat16, true>(s, a, nb, st) : bwd_t<__nv_bfloat16, false>(s, a, nb, st);
+    else
+      e = vec ? bwd_t<float, true>(s, a, nb, st) : bwd_t<float, false>(s, a, nb, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (dw || db) {      // no rows: the sums are zero (nb = 0)
+    k_norm_reduce<<<(2 * c.d + 31) / 32, dim3(32, 32), 0, st>>>(part, nb, c.d, dw, db, a.wbf16);
+    count_launch();
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace lh

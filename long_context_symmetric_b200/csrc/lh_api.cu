@@ -7,6 +7,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "k_diff.cuh"
 #include "lh_common.cuh"
 
 #ifndef LH_NO_NVTX
@@ -545,6 +546,197 @@ lh_status lh_cp_spread(const lh_config* cfg, int world, int rank, const float* d
   LH_REQ(dqs); LH_REQ(dks); LH_REQ(dvs); LH_REQ(slot_loc); LH_REQ(dq); LH_REQ(dk); LH_REQ(dv);
   LH_CUDA(launch_spread(shard_geom(g, world, rank), cfg->dtype, dqs, dks, dvs, slot_loc, dq, dk, dv,
                         (cudaStream_t)stream));
+  return LH_OK;
+}
+
+// ---------------------------------------------------------------- layer norm
+
+namespace {
+lh_status check_norm(const lh_norm_config* c) {
+  if (!c) return LH_ERR_NULL;
+  if ((c->dtype != LH_BF16 && c->dtype != LH_FP32) || (c->wdtype != LH_BF16 && c->wdtype != LH_FP32)) return LH_ERR_DTYPE;
+  if (c->M < 0 || c->M > (1LL << 40) || c->d < 1 || c->d > LH_NORM_MAX_D) return LH_ERR_SHAPE;
+  for (long long ld : {c->ldx, c->ldy})
+    if (ld != 0 && (ld < c->d || ld > (1LL << 40))) return LH_ERR_SHAPE;
+  if (!(c->eps >= 0.f) || std::isinf(c->eps)) return LH_ERR_SHAPE;
+  return LH_OK;
+}
+#define LH_OPT(p) do { if (!aligned16(p)) return LH_ERR_ALIGN; } while (0)
+}  // namespace
+
+lh_status lh_norm_plan(const lh_norm_config* cfg, size_t* ws_bytes) {
+  if (!ws_bytes) return LH_ERR_NULL;
+  lh_status st = check_norm(cfg);
+  if (st == LH_OK) *ws_bytes = norm_ws_bytes(*cfg);
+  return st;
+}
+
+lh_status lh_norm_fwd(const lh_norm_config* cfg, const void* x, const void* w, const void* b, void* y, float* mean,
+                      float* rstd, void* stream) {
+  LH_RANGE("lh_norm_fwd");
+  lh_status st = check_norm(cfg);
+  if (st != LH_OK) return st;
+  if (cfg->M == 0) return LH_OK;
+  LH_REQ(x); LH_REQ(y); LH_OPT(w); LH_OPT(b); LH_OPT(mean); LH_OPT(rstd);
+  LH_CUDA(launch_norm_fwd(*cfg, x, w, b, y, mean, rstd, (cudaStream_t)stream));
+  return LH_OK;
+}
+
+lh_status lh_norm_bwd(const lh_norm_config* cfg, const void* dy, const void* x, const void* w, const float* mean,
+                      const float* rstd, void* dx, void* dw, void* db, void* ws, size_t ws_bytes, void* stream) {
+  LH_RANGE("lh_norm_bwd");
+  lh_status st = check_norm(cfg);
+  if (st != LH_OK) return st;
+  LH_OPT(w); LH_OPT(dw); LH_OPT(db);
+  if (cfg->M > 0) {
+    LH_REQ(dy); LH_REQ(x); LH_REQ(mean); LH_REQ(rstd); LH_REQ(dx);
+    if (dw || db) {
+      LH_REQ(ws);
+      if (ws_bytes < norm_ws_bytes(*cfg)) return LH_ERR_WORKSPACE;
+    }
+  }
+  LH_CUDA(launch_norm_bwd(*cfg, dy, x, w, mean, rstd, dx, dw, db, (float*)ws, (cudaStream_t)stream));
+  return LH_OK;
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+lh_status lh_rope(const lh_rope_config* c, const void* q, const void* k, const void* pos, const double* freq,
+                  const int32_t* axis, int inverse, void* qo, void* ko, void* stream) {
+  LH_RANGE("lh_rope");
+  if (!c) return LH_ERR_NULL;
+  if (c->dtype != LH_BF16 && c->dtype != LH_FP32) return LH_ERR_DTYPE;
+  if ((unsigned)c->pairs > LH_ROPE_NEXT || (unsigned)c->pos64 > 1u) return LH_ERR_MODE;
+  if (c->B < 0 || c->N < 0 || (long long)c->B * c->N >= (1LL << 32)) return LH_ERR_SHAPE;
+  if (c->H < 1 || c->Hk < 0 || c->H > (1 << 15) || c->Hk > (1 << 15)) return LH_ERR_SHAPE;
+  if (c->D < 2 || c->D > LH_ROPE_MAX_D || c->rot < 2 || c->rot > c->D || c->rot % 2) return LH_ERR_SHAPE;
+  if (c->axes < 1 || c->axes > LH_ROPE_MAX_AXES) return LH_ERR_SHAPE;
+  const long long wq = (long long)c->H * c->D, wk = (long long)c->Hk * c->D, big = 1LL << 40;
+  for (long long ld : {c->q_ld, c->qo_ld})
+    if (ld != 0 && (ld < wq || ld > big)) return LH_ERR_SHAPE;
+  for (long long ld : {c->k_ld, c->ko_ld})
+    if (ld != 0 && (ld < wk || ld > big)) return LH_ERR_SHAPE;
+  for (long long s : {c->q_bs, c->k_bs, c->qo_bs, c->ko_bs, c->pos_as, c->pos_bs})
+    if (s < 0 || s > (1LL << 44)) return LH_ERR_SHAPE;
+  if ((long long)c->B * c->N == 0) return LH_OK;
+  LH_REQ(q); LH_REQ(qo); LH_REQ(pos); LH_REQ(freq); LH_REQ(axis);
+  if (c->Hk) { LH_REQ(k); LH_REQ(ko); }
+  int* err = device_error_ptr();
+  if (!err) return LH_ERR_CUDA;
+  LH_CUDA(launch_rope(*c, q, k, pos, freq, axis, inverse, qo, ko, err, (cudaStream_t)stream));
+  return LH_OK;
+}
+
+// ---------------------------------------------------------------- differential attention
+
+namespace {
+
+struct DiffSizes {
+  size_t tiles, lse, om, saved;         // offsets into `saved`, and its size
+  size_t delta, part, ws;              // offsets into the scratch, and its size
+};
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+lh_status make_diff(const lh_diff_config* c, DiffGeom* g, DiffSizes* z) {
+  if (!c) return LH_ERR_NULL;
+  if (c->dtype != LH_BF16 && c->dtype != LH_FP32) return LH_ERR_DTYPE;
+  if ((unsigned)c->packed > 1u || (unsigned)c->train > 1u) return LH_ERR_MODE;
+  if (c->B < 1 || c->B > (1 << 20) || c->T < 0 || c->T >= (1 << 30)) return LH_ERR_SHAPE;
+  if (c->H < 1 || c->H > (1 << 15) || c->Hk < 1 || c->H % c->Hk || (c->D != 64 && c->D != 128)) return LH_ERR_SHAPE;
+  if (!c->packed && c->T % c->B) return LH_ERR_SHAPE;
+  const long long wq = (long long)c->H * c->D, wk = (long long)c->Hk * c->D;
+  for (long long ld : {c->ldq, c->ldo})
+    if (ld != 0 && (ld < wq || ld % 8 || ld > (1LL << 40))) return LH_ERR_SHAPE;
+  for (long long ld : {c->ldk, c->ldv})
+    if (ld != 0 && (ld < wk || ld % 8 || ld > (1LL << 40))) return LH_ERR_SHAPE;
+  std::memset(g, 0, sizeof(*g));
+  g->B = c->B; g->T = c->T; g->H = c->H; g->Hk = c->Hk; g->G = c->H / c->Hk; g->D = c->D;
+  g->N = c->T / c->B;
+  g->ldq = c->ldq ? c->ldq : wq;
+  g->ldk = c->ldk ? c->ldk : wk;
+  g->ldv = c->ldv ? c->ldv : wk;
+  g->ldo = c->ldo ? c->ldo : wq;
+  std::memset(z, 0, sizeof(*z));
+  const size_t T = c->T, H = c->H, D = c->D;
+  g->ntile = diff_ntile(c->T, c->B, kDiffTileFP);
+  size_t at = up256((size_t)(g->ntile + 1) * sizeof(DiffTile));
+  if (c->train) {
+    z->lse = at; at += up256(2 * H * T * 4);
+    z->om = at; at += up256(2 * T * H * D * 4);
+  }
+  z->saved = at;
+  if (c->train) {
+    z->delta = 0;
+    z->part = up256(2 * H * T * 4);
+    z->ws = z->part + up256(H * ((T + kDiffDeltaRows - 1) / kDiffDeltaRows) * 4);
+  }
+  return LH_OK;
+}
+
+}  // namespace
+
+lh_status lh_diff_plan(const lh_diff_config* cfg, lh_diff_plan_t* out) {
+  if (!out) return LH_ERR_NULL;
+  DiffGeom g;
+  DiffSizes z;
+  lh_status st = make_diff(cfg, &g, &z);
+  if (st != LH_OK) return st;
+  out->saved_bytes = z.saved;
+  out->ws_bytes = z.ws;
+  return LH_OK;
+}
+
+lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void* k, const void* v, const void* lam,
+                           const int32_t* cu, void* o, void* saved, size_t saved_bytes, void* stream) {
+  LH_RANGE("lh_diff_attn_fwd");
+  DiffGeom g;
+  DiffSizes z;
+  lh_status st = make_diff(cfg, &g, &z);
+  if (st != LH_OK) return st;
+  if (cfg->packed ? !cu : cu != nullptr) return cu ? LH_ERR_MODE : LH_ERR_NULL;
+  if (g.T == 0) return LH_OK;
+  LH_REQ(q); LH_REQ(k); LH_REQ(v); LH_REQ(lam); LH_REQ(o); LH_REQ(saved);
+  if (saved_bytes < z.saved) return LH_ERR_WORKSPACE;
+  g.cu = cu;
+  int* err = device_error_ptr();
+  if (!err) return LH_ERR_CUDA;
+  char* sv = static_cast<char*>(saved);
+  cudaStream_t s = (cudaStream_t)stream;
+  DiffTile* tiles = reinterpret_cast<DiffTile*>(sv + z.tiles);
+  float* lse = cfg->train ? reinterpret_cast<float*>(sv + z.lse) : nullptr;
+  float* om = cfg->train ? reinterpret_cast<float*>(sv + z.om) : nullptr;
+  LH_CUDA(launch_diff_tiles(g, kDiffTileFP, tiles, err, s));
+  LH_CUDA(launch_diff_fwd_fp(g, cfg->dtype, q, k, v, lam, tiles, o, om, lse, s));
+  return LH_OK;
+}
+
+lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const void* q, const void* k, const void* v,
+                           const void* lam, const int32_t* cu, const void* saved, size_t saved_bytes,
+                           void* ws, size_t ws_bytes, void* dq, void* dk, void* dv, void* dlam, void* stream) {
+  LH_RANGE("lh_diff_attn_bwd");
+  DiffGeom g;
+  DiffSizes z;
+  lh_status st = make_diff(cfg, &g, &z);
+  if (st != LH_OK) return st;
+  if (!cfg->train) return LH_ERR_MODE;
+  if (cfg->packed ? !cu : cu != nullptr) return cu ? LH_ERR_MODE : LH_ERR_NULL;
+  LH_REQ(dlam);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (g.T == 0) {
+    LH_CUDA(launch_diff_dlam(g.H, 0, nullptr, cfg->dtype, dlam, s));
+    return LH_OK;
+  }
+  LH_REQ(dout); LH_REQ(q); LH_REQ(k); LH_REQ(v); LH_REQ(lam); LH_REQ(saved); LH_REQ(ws);
+  LH_REQ(dq); LH_REQ(dk); LH_REQ(dv);
+  if (saved_bytes < z.saved || ws_bytes < z.ws) return LH_ERR_WORKSPACE;
+  g.cu = cu;
+  const char* sv = static_cast<const char*>(saved);
+  char* w = static_cast<char*>(ws);
+  LH_CUDA(launch_diff_bwd_fp(g, cfg->dtype, dout, q, k, v, lam, reinterpret_cast<const DiffTile*>(sv + z.tiles),
+                             reinterpret_cast<const float*>(sv + z.om), reinterpret_cast<const float*>(sv + z.lse),
+                             reinterpret_cast<float*>(w + z.delta), reinterpret_cast<float*>(w + z.part), dq, dk, dv,
+                             dlam, s));
   return LH_OK;
 }
 

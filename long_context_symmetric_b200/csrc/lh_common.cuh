@@ -284,5 +284,12 @@ cudaError_t launch_attn_fwd(const Geom& g, lh_dtype dt, const void* qs, const vo
 cudaError_t launch_attn_bwd(const Geom& g, lh_dtype dt, const void* qs, const void* ks,
                             const void* vs, const void* dos, const float* lse, const float* delta,
                             const uint32_t* scale, float* dqs, float* dks, float* dvs, int* err, cudaStream_t s);
+size_t norm_ws_bytes(const lh_norm_config& c);
+cudaError_t launch_norm_fwd(const lh_norm_config& c, const void* x, const void* w, const void* b, void* y,
+                            float* mean, float* rstd, cudaStream_t s);
+cudaError_t launch_norm_bwd(const lh_norm_config& c, const void* dy, const void* x, const void* w, const float* mean,
+                            const float* rstd, void* dx, void* dw, void* db, float* part, cudaStream_t s);
+cudaError_t launch_rope(const lh_rope_config& c, const void* q, const void* k, const void* pos, const double* freq,
+                        const int32_t* axis, int inverse, void* qo, void* ko, int* err, cudaStream_t s);
 void count_launch(int n = 1);
 }  // namespace lh

@@ -66,6 +66,27 @@ class Buffers(ctypes.Structure):
                 ("dqs", c_void_p), ("dks", c_void_p), ("dvs", c_void_p), ("scale", c_void_p)]
 
 
+class NormConfig(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_longlong), ("d", c_int), ("dtype", c_int), ("wdtype", c_int),
+                ("ldx", ctypes.c_longlong), ("ldy", ctypes.c_longlong), ("eps", ctypes.c_float)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("H", c_int), ("Hk", c_int), ("D", c_int), ("rot", c_int), ("axes", c_int),
+                ("dtype", c_int), ("pairs", c_int), ("pos64", c_int)] + [
+                    (n, ctypes.c_longlong) for n in ("q_ld", "q_bs", "k_ld", "k_bs", "qo_ld", "qo_bs", "ko_ld", "ko_bs",
+                                                     "pos_as", "pos_bs")]
+
+
+class DiffConfig(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("H", c_int), ("Hk", c_int), ("D", c_int), ("dtype", c_int),
+                ("packed", c_int), ("train", c_int)] + [(n, ctypes.c_longlong) for n in ("ldq", "ldk", "ldv", "ldo")]
+
+
+class DiffPlan(ctypes.Structure):
+    _fields_ = [("saved_bytes", c_size_t), ("ws_bytes", c_size_t)]
+
+
 _lib = None
 
 _SIGS = {
@@ -99,6 +120,14 @@ _SIGS = {
     "lh_cp_scatter": ([ctypes.POINTER(Config), c_int, c_int] + [c_void_p] * 4, c_int),
     "lh_cp_scatter_bwd": ([ctypes.POINTER(Config), c_int, c_int] + [c_void_p] * 8, c_int),
     "lh_cp_attn_bwd": ([ctypes.POINTER(Config), c_int, c_int] + [c_void_p] * 12, c_int),
+    "lh_norm_plan": ([ctypes.POINTER(NormConfig), ctypes.POINTER(c_size_t)], c_int),
+    "lh_norm_fwd": ([ctypes.POINTER(NormConfig)] + [c_void_p] * 7, c_int),
+    "lh_norm_bwd": ([ctypes.POINTER(NormConfig)] + [c_void_p] * 9 + [c_size_t, c_void_p], c_int),
+    "lh_rope": ([ctypes.POINTER(RopeConfig)] + [c_void_p] * 5 + [c_int] + [c_void_p] * 3, c_int),
+    "lh_diff_plan": ([ctypes.POINTER(DiffConfig), ctypes.POINTER(DiffPlan)], c_int),
+    "lh_diff_attn_fwd": ([ctypes.POINTER(DiffConfig)] + [c_void_p] * 7 + [c_size_t, c_void_p], c_int),
+    "lh_diff_attn_bwd": ([ctypes.POINTER(DiffConfig)] + [c_void_p] * 7 + [c_size_t, c_void_p, c_size_t] +
+                         [c_void_p] * 5, c_int),
     "lh_cp_spread": ([ctypes.POINTER(Config), c_int, c_int] + [c_void_p] * 8, c_int),
 }
 
@@ -384,3 +413,344 @@ class LighthouseAttention(torch.autograd.Function):
 
 def lighthouse_attention(q, k, v, p: int, L: int, K: int, accum: str = "fp"):
     return LighthouseAttention.apply(q, k, v, p, L, K, accum)
+
+
+# ---------------------------------------------------------------------------
+# operators of the layer around the attention: layer norm, rotary positions,
+# differential attention
+# ---------------------------------------------------------------------------
+
+_DTYPES = {"bf16": LH_BF16, "fp32": LH_FP32}
+_TORCH = {LH_BF16: torch.bfloat16, LH_FP32: torch.float32}
+_NAMES = {torch.bfloat16: "bf16", torch.float32: "fp32"}
+
+
+def _call(name, dev, stream, *args):
+    """One entry point, on the device that the tensors live on."""
+    f = getattr(lib(), name)
+    if dev.index is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(stream))
+    else:
+        st = f(*args, _stream(stream))
+    if st != 0:
+        raise LHError(st, name)
+
+
+def _need(name, dev, *tensors):
+    """Each (label, tensor or None, dtype, elements): contiguous, of that type and at least that size."""
+    for label, t, dt, n in tensors:
+        if t is None:
+            continue
+        if t.dtype != dt:
+            raise ValueError(f"{name}: {label} has type {t.dtype}, {dt} is wanted")
+        if t.device != dev:
+            raise ValueError(f"{name}: {label} is on {t.device}, the call is on {dev}")
+        if t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{name}: {label} of shape {tuple(t.shape)}: {n} contiguous elements are wanted")
+
+
+def _span(t):
+    """Elements from a tensor's first one to the end of its storage."""
+    return t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+
+
+def _rows_fit(name, label, t, dt, dev, rows, ld, width):
+    """rows x width elements, ld apart, lie in the tensor's storage."""
+    if t.dtype != dt:
+        raise ValueError(f"{name}: {label} has type {t.dtype}, {dt} is wanted")
+    if t.device != dev:
+        raise ValueError(f"{name}: {label} is on {t.device}, the call is on {dev}")
+    if rows and (rows - 1) * ld + width > _span(t):
+        raise ValueError(f"{name}: {label} ends before row {rows - 1} of {width} elements, {ld} apart")
+
+
+def make_norm_config(M, d, dtype="bf16", wdtype=None, eps=1e-5, ldx=0, ldy=0) -> NormConfig:
+    """M rows of d values; ldx (ldy): elements between rows of x and dx (y and dy), 0: d."""
+    return NormConfig(M, d, _DTYPES[dtype], _DTYPES[wdtype or dtype], ldx, ldy, eps)
+
+
+def norm_ws_bytes(cfg: NormConfig) -> int:
+    n = c_size_t(0)
+    _check(lib().lh_norm_plan(ctypes.byref(cfg), ctypes.byref(n)), "lh_norm_plan")
+    return n.value
+
+
+def norm_workspace(cfg: NormConfig, device):
+    """Scratch of norm_bwd (any buffer of norm_ws_bytes(cfg) bytes serves)."""
+    return torch.empty(max(norm_ws_bytes(cfg), 16), dtype=torch.uint8, device=device)
+
+
+def norm_fwd(cfg, x, w, b, y, mean=None, rstd=None, stream=None):
+    dev, dt, wt, M, d = x.device, _TORCH[cfg.dtype], _TORCH[cfg.wdtype], cfg.M, cfg.d
+    _rows_fit("lh_norm_fwd", "x", x, dt, dev, M, cfg.ldx or d, d)
+    _rows_fit("lh_norm_fwd", "y", y, dt, dev, M, cfg.ldy or d, d)
+    _need("lh_norm_fwd", dev, ("w", w, wt, d), ("b", b, wt, d), ("mean", mean, torch.float32, M),
+          ("rstd", rstd, torch.float32, M))
+    _call("lh_norm_fwd", dev, stream, ctypes.byref(cfg), _p(x), _p(w), _p(b), _p(y), _p(mean), _p(rstd))
+
+
+def norm_bwd(cfg, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
+    dev, dt, wt, M, d = x.device, _TORCH[cfg.dtype], _TORCH[cfg.wdtype], cfg.M, cfg.d
+    _rows_fit("lh_norm_bwd", "x", x, dt, dev, M, cfg.ldx or d, d)
+    _rows_fit("lh_norm_bwd", "dx", dx, dt, dev, M, cfg.ldx or d, d)
+    _rows_fit("lh_norm_bwd", "dy", dy, dt, dev, M, cfg.ldy or d, d)
+    _need("lh_norm_bwd", dev, ("w", w, wt, d), ("mean", mean, torch.float32, M), ("rstd", rstd, torch.float32, M),
+          ("dw", dw, wt, d), ("db", db, wt, d))
+    _call("lh_norm_bwd", dev, stream, ctypes.byref(cfg), _p(dy), _p(x), _p(w), _p(mean), _p(rstd), _p(dx), _p(dw),
+          _p(db), _p(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+
+
+ROPE_PAIRS = {"half": 0, "next": 1}
+
+
+def make_rope_config(B, N, H, Hk, D, rot=None, axes=1, dtype="bf16", pairs="half", pos64=False, shared_pos=False,
+                     q_ld=0, q_bs=0, k_ld=0, k_bs=0, qo_ld=0, qo_bs=0, ko_ld=0, ko_bs=0, pos_as=None,
+                     pos_bs=None) -> RopeConfig:
+    """q [B][N][H][D] and k [B][N][Hk][D], the first `rot` elements of a row rotated; positions [axes][B][N]
+    ([axes][N] if the sequences share them). *_ld, *_bs: elements between tokens and sequences, 0: contiguous."""
+    return RopeConfig(B, N, H, Hk, D, D if rot is None else rot, axes, _DTYPES[dtype], ROPE_PAIRS[pairs], int(pos64),
+                      q_ld, q_bs, k_ld, k_bs, qo_ld, qo_bs, ko_ld, ko_bs,
+                      (N if shared_pos else B * N) if pos_as is None else pos_as,
+                      (0 if shared_pos else N) if pos_bs is None else pos_bs)
+
+
+def rope(cfg, q, k, pos, freq, axis, qo, ko, inverse=False, stream=None):
+    """qo, ko: q and k rotated (q and k themselves: in place). inverse: the backward pass, dq and dk for q and k."""
+    dev, dt, B, N, D = q.device, _TORCH[cfg.dtype], cfg.B, cfg.N, cfg.D
+    if B and N:
+        for label, t, heads, ld, bs in (("q", q, cfg.H, cfg.q_ld, cfg.q_bs), ("qo", qo, cfg.H, cfg.qo_ld, cfg.qo_bs),
+                                        ("k", k, cfg.Hk, cfg.k_ld, cfg.k_bs), ("ko", ko, cfg.Hk, cfg.ko_ld, cfg.ko_bs)):
+            if heads:
+                ld = ld or heads * D
+                _rows_fit("lh_rope", label, t, dt, dev, 1, 0, (B - 1) * (bs or N * ld) + (N - 1) * ld + heads * D)
+        _rows_fit("lh_rope", "pos", pos, torch.int64 if cfg.pos64 else torch.int32, dev, 1, 0,
+                  (cfg.axes - 1) * cfg.pos_as + (B - 1) * cfg.pos_bs + N)
+    _need("lh_rope", dev, ("freq", freq, torch.float64, cfg.rot // 2), ("axis", axis, torch.int32, cfg.rot // 2))
+    _call("lh_rope", dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(pos), _p(freq), _p(axis), int(inverse), _p(qo), _p(ko))
+
+
+def make_diff_config(B, N, H, D, dtype="bf16", Hk=None, rows=None, train=True, ldq=0, ldk=0, ldv=0, ldo=0) -> DiffConfig:
+    """B sequences of N tokens, H query heads of D elements (two maps of D/2) on Hk key/value heads. rows: B
+    sequences packed in that many token rows, their offsets given to each call as cu (N is then not used)."""
+    return DiffConfig(B, B * N if rows is None else rows, H, H if Hk is None else Hk, D, _DTYPES[dtype],
+                      int(rows is not None), int(train), ldq, ldk, ldv, ldo)
+
+
+def diff_plan(cfg: DiffConfig) -> DiffPlan:
+    out = DiffPlan()
+    _check(lib().lh_diff_plan(ctypes.byref(cfg), ctypes.byref(out)), "lh_diff_plan")
+    return out
+
+
+class DiffWorkspace:
+    """Buffers of one differential attention: what the forward pass leaves for the backward, and the backward's
+    scratch. One forward + backward at a time: calls that overlap each need their own."""
+
+    def __init__(self, cfg: DiffConfig, device):
+        self.plan = pl = diff_plan(cfg)
+        self.saved = torch.empty(max(pl.saved_bytes, 16), dtype=torch.uint8, device=device)
+        self.ws = torch.empty(max(pl.ws_bytes, 16), dtype=torch.uint8, device=device) if cfg.train else None
+
+
+def _diff_check(name, cfg, cu, dev, qs, ks):
+    dt, D = _TORCH[cfg.dtype], cfg.D
+    for label, t, ld, heads in qs + ks:
+        _rows_fit(name, label, t, dt, dev, cfg.T, ld or heads * D, heads * D)
+    if cfg.packed:
+        if cu is None:
+            raise ValueError(f"{name}: packed sequences need cu")
+        _need(name, dev, ("cu", cu, torch.int32, cfg.B + 1))
+
+
+def diff_attn_fwd(cfg, q, k, v, lam, o, ws: DiffWorkspace, cu=None, stream=None):
+    dev = q.device
+    _diff_check("lh_diff_attn_fwd", cfg, cu, dev, [("q", q, cfg.ldq, cfg.H), ("o", o, cfg.ldo, cfg.H)],
+                [("k", k, cfg.ldk, cfg.Hk), ("v", v, cfg.ldv, cfg.Hk)])
+    _need("lh_diff_attn_fwd", dev, ("lam", lam, _TORCH[cfg.dtype], cfg.H), ("saved", ws.saved, torch.uint8, 0))
+    _call("lh_diff_attn_fwd", dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(v), _p(lam), _p(cu), _p(o),
+          _p(ws.saved), ws.saved.numel())
+
+
+def diff_attn_bwd(cfg, dout, q, k, v, lam, ws: DiffWorkspace, dq, dk, dv, dlam, cu=None, stream=None):
+    dev = q.device
+    _diff_check("lh_diff_attn_bwd", cfg, cu, dev,
+                [("q", q, cfg.ldq, cfg.H), ("dq", dq, cfg.ldq, cfg.H), ("dout", dout, cfg.ldo, cfg.H)],
+                [("k", k, cfg.ldk, cfg.Hk), ("dk", dk, cfg.ldk, cfg.Hk), ("v", v, cfg.ldv, cfg.Hk),
+                 ("dv", dv, cfg.ldv, cfg.Hk)])
+    dt = _TORCH[cfg.dtype]
+    _need("lh_diff_attn_bwd", dev, ("lam", lam, dt, cfg.H), ("dlam", dlam, dt, cfg.H),
+          ("saved", ws.saved, torch.uint8, 0), ("ws", ws.ws, torch.uint8, 0))
+    _call("lh_diff_attn_bwd", dev, stream, ctypes.byref(cfg), _p(dout), _p(q), _p(k), _p(v), _p(lam), _p(cu),
+          _p(ws.saved), ws.saved.numel(), _p(ws.ws), ws.ws.numel() if ws.ws is not None else 0, _p(dq), _p(dk),
+          _p(dv), _p(dlam))
+
+
+def _name(t, what):
+    if t.dtype not in _NAMES:
+        raise ValueError(f"{what}: {t.dtype} is not supported (bfloat16, float32)")
+    return _NAMES[t.dtype]
+
+
+def _whole(t):
+    """Contiguous and 16-byte aligned."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class LayerNorm(torch.autograd.Function):
+    """y = layer norm of the last axis of x, weight w and bias b (either None)."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, eps: float):
+        d = x.shape[-1]
+        for label, t in (("w", w), ("b", b)):
+            if t is not None and tuple(t.shape) != (d,):
+                raise ValueError(f"layer_norm: {label} has shape {tuple(t.shape)}, ({d},) is wanted")
+        if w is not None and b is not None and w.dtype != b.dtype:
+            raise ValueError("layer_norm: w and b have unlike types")
+        x = _whole(x)
+        w, b = (None if t is None else _whole(t) for t in (w, b))
+        p = w if w is not None else b
+        M = x.numel() // d if d else 0
+        cfg = make_norm_config(M, d, _name(x, "layer_norm"), _name(x if p is None else p, "layer_norm"), eps)
+        y = torch.empty_like(x)
+        mean, rstd = (torch.empty(M, dtype=torch.float32, device=x.device) for _ in range(2))
+        norm_fwd(cfg, x, w, b, y, mean, rstd)
+        ctx.save_for_backward(x, w, b, mean, rstd)
+        ctx.cfg = cfg
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, b, mean, rstd = ctx.saved_tensors
+        dy, dx = _whole(dy), torch.empty_like(x)
+        dw = torch.empty_like(w) if w is not None and ctx.needs_input_grad[1] else None
+        db = torch.empty_like(b) if b is not None and ctx.needs_input_grad[2] else None
+        norm_bwd(ctx.cfg, dy, x, w, mean, rstd, dx, dw, db, norm_workspace(ctx.cfg, x.device))
+        return dx, dw, db, None
+
+
+def layer_norm(x, w=None, b=None, eps: float = 1e-5):
+    return LayerNorm.apply(x, w, b, eps)
+
+
+class RopePlan:
+    """The device tables of a rotary embedding: a frequency (radians per position) and an axis for each pair.
+
+    sections: pairs per axis (their sum is rot/2; one axis: None). order: "runs" (the first sections[0] pairs turn
+    with axis 0, and so on) or "cycle" (pairs dealt to the axes in turn, an axis dropping out once it has its
+    share). ladder: "shared" (pair i has base^(-2i/rot), whatever its axis) or "own" (each axis has its own ladder
+    from 1 down, over its own pairs). freq: the frequencies themselves instead, for a scaled ladder."""
+
+    def __init__(self, rot, sections=None, base=10000.0, device="cuda", order="runs", ladder="shared", freq=None):
+        R = rot // 2
+        sections = [R] if sections is None else list(sections)
+        if rot < 2 or rot % 2 or sum(sections) != R or min(sections) < 0:
+            raise ValueError(f"RopePlan: sections {sections} do not add up to {rot}/2 pairs")
+        if order not in ("runs", "cycle") or ladder not in ("shared", "own"):
+            raise ValueError(f"RopePlan: unknown order {order!r} or ladder {ladder!r}")
+        axis, left = [], list(sections)
+        if order == "runs":
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        else:
+            while len(axis) < R:
+                for a, n in enumerate(left):
+                    if n:
+                        axis.append(a)
+                        left[a] -= 1
+        seen = [0] * len(sections)
+        own_place = []
+        for a in axis:
+            own_place.append(seen[a])
+            seen[a] += 1
+        if freq is None:
+            freq = [base ** (-2.0 * i / rot) if ladder == "shared" else base ** (-float(own_place[i]) / sections[axis[i]])
+                    for i in range(R)]
+        self.rot, self.axes = rot, len(sections)
+        self.freq = torch.as_tensor(freq, dtype=torch.float64).to(device)
+        self.axis = torch.tensor(axis, dtype=torch.int32, device=device)
+        if self.freq.shape != (R,):
+            raise ValueError(f"RopePlan: {tuple(self.freq.shape)} frequencies, ({R},) are wanted")
+
+    def positions(self, pos, B, N):
+        """pos as [axes][B][N] or [axes][N] (shared by the sequences; [B][N], [N] with one axis), int32 or int64."""
+        if pos.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"rotary: positions have type {pos.dtype}, int32 or int64 are wanted")
+        if self.axes == 1 and (pos.ndim == 1 or (pos.ndim == 2 and tuple(pos.shape) == (B, N) != (1, N))):
+            pos = pos[None]
+        if tuple(pos.shape) not in ((self.axes, B, N), (self.axes, N)):
+            raise ValueError(f"rotary: positions of shape {tuple(pos.shape)} for {self.axes} axes, {B} x {N} tokens")
+        return _whole(pos)
+
+
+class Rotary(torch.autograd.Function):
+    """(q, k) rotated by their tokens' positions; the gradient turns back."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, plan: RopePlan, pairs: str):
+        B, N, H, D = q.shape
+        if k.shape[:2] != (B, N) or k.shape[3] != D or k.dtype != q.dtype:
+            raise ValueError(f"rotary: q {tuple(q.shape)} {q.dtype} and k {tuple(k.shape)} {k.dtype} do not belong together")
+        q, k, pos = _whole(q), _whole(k), plan.positions(pos, B, N)
+        cfg = make_rope_config(B, N, H, k.shape[2], D, plan.rot, plan.axes, _name(q, "rotary"), pairs,
+                               pos64=pos.dtype == torch.int64, shared_pos=pos.ndim == 2)
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        rope(cfg, q, k, pos, plan.freq, plan.axis, qo, ko)
+        ctx.cfg, ctx.plan = cfg, plan
+        ctx.save_for_backward(pos)
+        return qo, ko
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        (pos,) = ctx.saved_tensors
+        dq, dk = _whole(dq), _whole(dk)
+        gq, gk = torch.empty_like(dq), torch.empty_like(dk)
+        rope(ctx.cfg, dq, dk, pos, ctx.plan.freq, ctx.plan.axis, gq, gk, inverse=True)
+        return gq, gk, None, None, None
+
+
+def rotary(q, k, pos, plan: RopePlan, pairs: str = "half"):
+    """q [B, N, H, D], k [B, N, Hk, D] rotated by positions pos (see RopePlan.positions)."""
+    return Rotary.apply(q, k, pos, plan, pairs)
+
+
+class DifferentialAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lam, cu):
+        packed = cu is not None
+        if q.ndim != (3 if packed else 4) or k.shape != v.shape or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+            raise ValueError(f"differential_attention: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not "
+                             f"belong together ([B, N, heads, D], or [T, heads, D] with cu)")
+        H, D = q.shape[-2:]
+        Hk = k.shape[-2]
+        if any(t.dtype != q.dtype for t in (k, v, lam)) or tuple(lam.shape) != (H,):
+            raise ValueError("differential_attention: k, v and lam [H] have q's type")
+        q, k, v, lam = (_whole(t) for t in (q, k, v, lam))
+        name = _name(q, "differential_attention")
+        cfg = (make_diff_config(cu.numel() - 1, 0, H, D, name, Hk, rows=q.shape[0]) if packed
+               else make_diff_config(q.shape[0], q.shape[1], H, D, name, Hk))
+        ws = DiffWorkspace(cfg, q.device)
+        # packed: rows outside the sequences are not written by the kernels
+        o = torch.zeros_like(q) if packed else torch.empty_like(q)
+        diff_attn_fwd(cfg, q, k, v, lam, o, ws, cu=cu)
+        ctx.cfg, ctx.ws = cfg, ws
+        ctx.save_for_backward(q, k, v, lam, cu)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, lam, cu = ctx.saved_tensors
+        new = torch.zeros_like if ctx.cfg.packed else torch.empty_like
+        dq, dk, dv, dlam = new(q), new(k), new(v), torch.empty_like(lam)
+        diff_attn_bwd(ctx.cfg, _whole(do), q, k, v, lam, ctx.ws, dq, dk, dv, dlam, cu=cu)
+        return dq, dk, dv, dlam, None
+
+
+def differential_attention(q, k, v, lam, cu=None):
+    """o = (softmax map 1 - lam * softmax map 2) v, causal; q [B, N, H, D], k, v [B, N, Hk, D], lam [H]. With cu
+    (int32 [sequences + 1], device): q [T, H, D] and so on, the sequences packed one behind the other."""
+    return DifferentialAttention.apply(q, k, v, lam, cu)
