@@ -13,7 +13,7 @@ __device__ __forceinline__ int seq_tiles(const DiffGeom& g, int b, int ts) {
 // One block per sequence. The tile with index i of sequence b comes behind all
 // tiles with a larger index and behind the tiles with index i of the sequences
 // before b: rank = sum over b' of max(0, n_b' - 1 - i) + #{b' < b: n_b' > i}.
-__global__ void k_diff_tiles(const DiffGeom g, int ts, DiffTile* tiles, int* err) {
+__global__ void k_diff_tiles(const DiffGeom g, int ts, DiffTile* tiles, int* seq, uint32_t* amax, int* err) {
   const int b = blockIdx.x;
   int lo, hi;
   diff_seq(g, b, lo, hi);
@@ -21,6 +21,8 @@ __global__ void k_diff_tiles(const DiffGeom g, int ts, DiffTile* tiles, int* err
     const int c0 = g.cu[b], c1 = g.cu[b + 1];
     if (c0 < 0 || c1 < c0 || c1 > g.T) report_error(err, LH_ERR_DEVICE, 402);
   }
+  if (amax)
+    for (int i = threadIdx.x; i < 3 * g.Hk; i += blockDim.x) amax[((size_t)(i / g.Hk) * g.B + b) * g.Hk + i % g.Hk] = 0;
   const int n = (hi - lo + ts - 1) / ts;
   const int pad = (lo + ts - 1) / ts * ts + b * ts;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -33,7 +35,10 @@ __global__ void k_diff_tiles(const DiffGeom g, int ts, DiffTile* tiles, int* err
     } else {
       rank = (long long)g.B * (n - 1 - i) + b;
     }
-    if (rank < g.ntile) tiles[rank] = make_int4(lo, hi - lo, pad, i);
+    if (rank < g.ntile) {
+      tiles[rank] = make_int4(lo, hi - lo, pad, i);
+      if (seq) seq[rank] = b;
+    }
   }
   if (b == 0) {
     __shared__ int total;
@@ -67,8 +72,9 @@ __global__ void __launch_bounds__(256) k_diff_dlam(int n, const float* __restric
 
 }  // namespace
 
-cudaError_t launch_diff_tiles(const DiffGeom& g, int ts, DiffTile* tiles, int* err, cudaStream_t s) {
-  k_diff_tiles<<<g.B, 256, 0, s>>>(g, ts, tiles, err);
+cudaError_t launch_diff_tiles(const DiffGeom& g, int ts, DiffTile* tiles, int* seq, uint32_t* amax, int* err,
+                              cudaStream_t s) {
+  k_diff_tiles<<<g.B, 256, 0, s>>>(g, ts, tiles, seq, amax, err);
   count_launch();
   return cudaGetLastError();
 }

@@ -47,7 +47,9 @@ __device__ __forceinline__ void diff_seq(const DiffGeom& g, int b, int& lo, int&
   }
 }
 
-cudaError_t launch_diff_tiles(const DiffGeom& g, int ts, DiffTile* tiles, int* err, cudaStream_t s);
+// seq (NULL: not wanted): the sequence of each entry; amax: [3][B][Hk], set to zero
+cudaError_t launch_diff_tiles(const DiffGeom& g, int ts, DiffTile* tiles, int* seq, uint32_t* amax, int* err,
+                              cudaStream_t s);
 // dlam[h] = -(sum of the n partial sums part[h][..]), rounded to dtype
 cudaError_t launch_diff_dlam(int H, int n, const float* part, lh_dtype dt, void* dlam, cudaStream_t s);
 

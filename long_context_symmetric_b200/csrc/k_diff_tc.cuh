@@ -1,0 +1,39 @@
+// Differential attention on the tensor cores: buffers and constants that the
+// forward and backward kernels share.
+#pragma once
+
+#include "k_diff.cuh"
+#include "tc_ptx.cuh"
+
+namespace lh {
+
+constexpr int kDSub = 128 * 64 * 2;   // one 128-row x 64-column 16-bit swizzle tile
+
+// Parts of the caller's buffers. Padded rows: g.ntile * 128 per head.
+struct DiffTC {
+  DiffTile* tiles;            // [ntile + 1]
+  int* seq;                   // [ntile]: the tile's sequence
+  uint32_t* amax;             // [3][B][Hk] largest magnitudes of q (over the query heads that share the
+                              // key/value head), k, v
+  __half *qs, *ks, *vs;       // [H | Hk][padded rows][D]
+  __half* om;                 // [H][2][padded rows][D]: A_m v 2^-ev
+  float* lse;                 // [H][2][padded rows], base 2
+  uint32_t* amax_do;          // [B][Hk], like q's
+  __half* dos;                // [H][padded rows][D]
+  float* delta;               // [H][2][padded rows]
+  float* part;                // [H][ntile] sums of delta 2
+};
+
+// 16-wide slice i of a K-major tile's rows, as an offset of its descriptor
+__device__ __forceinline__ uint64_t kslice(int i) {
+  return (uint64_t)((i >> 2) * (kDSub >> 4) + (i & 3) * 2);
+}
+
+bool make_tmap_16(CUtensorMap* m, const void* base, int D, int S, int BH, bool fp16, int box_rows);
+
+cudaError_t launch_diff_fwd_tc(const DiffGeom& g, const DiffTC& b, const void* q, const void* k, const void* v,
+                               const void* lam, void* o, int train, int* err, cudaStream_t s);
+cudaError_t launch_diff_bwd_tc(const DiffGeom& g, const DiffTC& b, const void* dout, const void* lam, void* dq, void* dk,
+                               void* dv, void* dlam, int* err, cudaStream_t s);
+
+}  // namespace lh

@@ -7,7 +7,7 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "k_diff.cuh"
+#include "k_diff_tc.cuh"
 #include "lh_common.cuh"
 
 #ifndef LH_NO_NVTX
@@ -632,8 +632,10 @@ lh_status lh_rope(const lh_rope_config* c, const void* q, const void* k, const v
 namespace {
 
 struct DiffSizes {
-  size_t tiles, lse, om, saved;         // offsets into `saved`, and its size
-  size_t delta, part, ws;              // offsets into the scratch, and its size
+  // parts of `saved`, and its size (seq .. vs: tensor cores)
+  size_t tiles, seq, amax, qs, ks, vs, lse, om, saved;
+  size_t delta, part, amax_do, dos, ws;        // parts of the scratch, and its size
+  int tc;
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -659,19 +661,56 @@ lh_status make_diff(const lh_diff_config* c, DiffGeom* g, DiffSizes* z) {
   g->ldo = c->ldo ? c->ldo : wq;
   std::memset(z, 0, sizeof(*z));
   const size_t T = c->T, H = c->H, D = c->D;
-  g->ntile = diff_ntile(c->T, c->B, kDiffTileFP);
-  size_t at = up256((size_t)(g->ntile + 1) * sizeof(DiffTile));
+  z->tc = c->dtype == LH_BF16 && !force_simt();
+  g->ntile = diff_ntile(c->T, c->B, z->tc ? kDiffTileTC : kDiffTileFP);
+  const size_t R = z->tc ? (size_t)g->ntile * kDiffTileTC : T, Hk = c->Hk;     // rows of the statistics
+  size_t at = 0;
+  auto part = [&at](size_t bytes) { const size_t p = at; at += up256(bytes); return p; };
+  z->tiles = part((size_t)(g->ntile + 1) * sizeof(DiffTile));
+  if (z->tc) {
+    z->seq = part((size_t)g->ntile * 4);
+    z->amax = part(3 * (size_t)c->B * Hk * 4);
+    z->qs = part(H * R * D * 2);
+    z->ks = part(Hk * R * D * 2);
+    z->vs = part(Hk * R * D * 2);
+  }
   if (c->train) {
-    z->lse = at; at += up256(2 * H * T * 4);
-    z->om = at; at += up256(2 * T * H * D * 4);
+    z->lse = part(2 * H * R * 4);
+    z->om = part(2 * H * R * D * (z->tc ? 2 : 4));
   }
   z->saved = at;
+  at = 0;
   if (c->train) {
-    z->delta = 0;
-    z->part = up256(2 * H * T * 4);
-    z->ws = z->part + up256(H * ((T + kDiffDeltaRows - 1) / kDiffDeltaRows) * 4);
+    z->delta = part(2 * H * R * 4);
+    z->part = part(H * (z->tc ? (size_t)g->ntile : (T + kDiffDeltaRows - 1) / kDiffDeltaRows) * 4);
+    if (z->tc) {
+      z->amax_do = part((size_t)c->B * Hk * 4);
+      z->dos = part(H * R * D * 2);
+    }
+    z->ws = at;
   }
   return LH_OK;
+}
+
+DiffTC diff_tc(const DiffSizes& z, void* saved, void* ws) {
+  char *s = static_cast<char*>(saved), *w = static_cast<char*>(ws);
+  DiffTC b;
+  std::memset(&b, 0, sizeof(b));
+  b.tiles = reinterpret_cast<DiffTile*>(s + z.tiles);
+  b.seq = reinterpret_cast<int*>(s + z.seq);
+  b.amax = reinterpret_cast<uint32_t*>(s + z.amax);
+  b.qs = reinterpret_cast<__half*>(s + z.qs);
+  b.ks = reinterpret_cast<__half*>(s + z.ks);
+  b.vs = reinterpret_cast<__half*>(s + z.vs);
+  b.lse = reinterpret_cast<float*>(s + z.lse);
+  b.om = reinterpret_cast<__half*>(s + z.om);
+  if (w) {
+    b.delta = reinterpret_cast<float*>(w + z.delta);
+    b.part = reinterpret_cast<float*>(w + z.part);
+    b.amax_do = reinterpret_cast<uint32_t*>(w + z.amax_do);
+    b.dos = reinterpret_cast<__half*>(w + z.dos);
+  }
+  return b;
 }
 
 }  // namespace
@@ -706,7 +745,11 @@ lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void*
   DiffTile* tiles = reinterpret_cast<DiffTile*>(sv + z.tiles);
   float* lse = cfg->train ? reinterpret_cast<float*>(sv + z.lse) : nullptr;
   float* om = cfg->train ? reinterpret_cast<float*>(sv + z.om) : nullptr;
-  LH_CUDA(launch_diff_tiles(g, kDiffTileFP, tiles, err, s));
+  if (z.tc) {
+    LH_CUDA(launch_diff_fwd_tc(g, diff_tc(z, saved, nullptr), q, k, v, lam, o, cfg->train, err, s));
+    return LH_OK;
+  }
+  LH_CUDA(launch_diff_tiles(g, kDiffTileFP, tiles, nullptr, nullptr, err, s));
   LH_CUDA(launch_diff_fwd_fp(g, cfg->dtype, q, k, v, lam, tiles, o, om, lse, s));
   return LH_OK;
 }
@@ -731,6 +774,12 @@ lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const vo
   LH_REQ(dq); LH_REQ(dk); LH_REQ(dv);
   if (saved_bytes < z.saved || ws_bytes < z.ws) return LH_ERR_WORKSPACE;
   g.cu = cu;
+  int* err = device_error_ptr();
+  if (!err) return LH_ERR_CUDA;
+  if (z.tc) {
+    LH_CUDA(launch_diff_bwd_tc(g, diff_tc(z, const_cast<void*>(saved), ws), dout, lam, dq, dk, dv, dlam, err, s));
+    return LH_OK;
+  }
   const char* sv = static_cast<const char*>(saved);
   char* w = static_cast<char*>(ws);
   LH_CUDA(launch_diff_bwd_fp(g, cfg->dtype, dout, q, k, v, lam, reinterpret_cast<const DiffTile*>(sv + z.tiles),
