@@ -18,8 +18,8 @@
 // k_diff_fwd_tc. One CTA per 128-row query tile and head; both maps share the
 // row, so the second stream of tiles that keeps the tensor core busy during a
 // softmax is the second map, and K and V tiles are loaded once for both.
-// 320 threads: warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 softmax of map
-// 1, warps 6-9 of map 2 (one thread per row and map). TMEM: S1, O1, S2, O2, 128
+// Three warpgroups: warp 0 TMA producer, warp 1 MMA issuer; warps 4-7 softmax of
+// map 1, warps 8-11 of map 2 (one thread per row and map). TMEM: S1, O1, S2, O2, 128
 // columns each. Per key tile j the issuer runs
 //   PV_1(j), S_1(j+1), PV_2(j), S_2(j+1)
 // (S_m: 128 x 128 x D/2, PV_m: 128 x D x 128, P_m as the TMEM operand in S_m's
@@ -40,9 +40,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kFwdThreads = 320;
 constexpr float kPBias = 7.f;       // P is held at 2^7 times its value
-constexpr float kLn2f = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- working copies
 
@@ -122,7 +120,7 @@ struct FwdBars {
 static_assert(sizeof(FwdBars) <= 256, "barrier block");
 
 template <int D>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kDiffThreads, 1)
 k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
               const __grid_constant__ CUtensorMap tv, const DiffGeom g, const __nv_bfloat16* __restrict__ lam,
               const DiffTile* __restrict__ tiles, const int* __restrict__ seq, const uint32_t* __restrict__ amax,
@@ -175,6 +173,7 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   const uint32_t tbase = bars->tmem_base;
   volatile Abort* ab = &bars->abort;
 
+  if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0) {
       int ik = 0, iv = 0;            // K / V tiles issued
@@ -263,9 +262,10 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     __syncwarp();
     Abort none{0};
     mbar_wait(&bars->drain, 0, &none, nullptr, 0);
-  } else {
+  } else if (warp >= 4) {
+    regs_take();
     // softmax of map m: one thread per query row / TMEM lane
-    const int m = (warp - 2) >> 2;
+    const int m = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t la = (uint32_t)(quarter * 32) << 16;
@@ -406,10 +406,12 @@ cudaError_t fwd_t(const DiffGeom& g, const DiffTC& b, const void* lam, void* o, 
     return cudaErrorInvalidValue;
   const int smem = FwdLayout<D>::BYTES;
   auto kern = k_diff_fwd_tc<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = diff_regs_ok(kern);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const float c2 = (float)(1.4426950408889634 / sqrt((double)(D / 2)));
-  kern<<<g.ntile * g.H, kFwdThreads, smem, s>>>(tq, tk, tv, g, (const __nv_bfloat16*)lam, b.tiles, b.seq, b.amax,
+  kern<<<g.ntile * g.H, kDiffThreads, smem, s>>>(tq, tk, tv, g, (const __nv_bfloat16*)lam, b.tiles, b.seq, b.amax,
                                                 (__nv_bfloat16*)o, train ? b.om : nullptr, train ? b.lse : nullptr, c2, err);
   count_launch();
   return cudaGetLastError();

@@ -24,6 +24,22 @@ struct DiffTC {
   float* part;                // [H][ntile] sums of delta 2
 };
 
+// Registers. A CTA of three warpgroups (384 threads) is launched with 168
+// registers a thread, all that a one-CTA SM has (launch bounds 384, 1). The
+// warpgroup of the producer and the issuer gives up 96 of them, each of the two
+// compute warpgroups takes 48 more: 72 + 2 * 216 = 3 * 168, so the split fits
+// the CTA's own allotment and no increase can wait for registers that never
+// come. diff_regs_ok makes sure of the 168 before the first launch.
+constexpr int kDiffThreads = 384, kDiffLaunchRegs = 168;
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+template <typename K>
+cudaError_t diff_regs_ok(K kern) {
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kern);
+  return e != cudaSuccess ? e : a.numRegs == kDiffLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 // 16-wide slice i of a K-major tile's rows, as an offset of its descriptor
 __device__ __forceinline__ uint64_t kslice(int i) {
   return (uint64_t)((i >> 2) * (kDSub >> 4) + (i & 3) * 2);

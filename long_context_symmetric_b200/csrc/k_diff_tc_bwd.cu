@@ -39,7 +39,6 @@ using namespace tc;
 
 constexpr int kStages = 3;
 constexpr int kComputeWarps = 8;
-constexpr int kThreads = 64 + 32 * kComputeWarps;
 constexpr uint32_t kX = 0, kY = 128, kAcc0 = 256, kAcc1 = 384;   // dkdv: X, Y, dV, dK
 constexpr uint32_t kQX2 = 128, kQY = 256, kQAcc = 384;           // dq: X_1 at 0, X_2, Y, dQ
 
@@ -300,7 +299,7 @@ __device__ __forceinline__ void ds_cols(const uint32_t (&p)[32], const uint32_t 
 
 // ---------------------------------------------------------------- dk, dv
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDiffThreads, 1)
 k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo, const DiffGeom g,
                const __nv_bfloat16* __restrict__ lam, const DiffTile* __restrict__ tiles, const int* __restrict__ seq,
@@ -322,7 +321,7 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   bwd_setup(bars, warp);
   const uint32_t tbase = bars->tmem_base;
   volatile Abort* ab = &bars->abort;
-
+  if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0)
       bwd_produce<D>(sm, bars, &tk, &tv, tl.z + j * 128, hk, &tq, &tdo, tl.z + j * 128, per, hk * g.G, n, ab, err);
@@ -376,16 +375,17 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       }
     }
     is.finish(ok);
-  } else {
+  } else if (warp >= 4) {
+    regs_take();
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;                   // which 64 of the 128 columns
+    const int half = (warp - 4) >> 2;                   // which 64 of the 128 columns
     const int m = quarter * 32 + lane;                  // key row within the tile / TMEM lane
     const uint32_t la = (uint32_t)(quarter * 32) << 16;
     const uint32_t cX = tbase + la + kX + 64 * half, cY = tbase + la + kY + 64 * half;
     // the statistics of this half's 64 query columns: [0] -lse 1, [1] -lse 2 (+ sp),
     // [2] -d1, [3] -d2 in dS units; thread hid fetches rows hid / 64 and 2 + hid / 64
     float* vec = reinterpret_cast<float*>(smem_raw + 256) + 256 * half;
-    const int hid = (threadIdx.x - 64) & 127, vr = hid >> 6, vc = hid & 63;
+    const int hid = threadIdx.x & 127, vr = hid >> 6, vc = hid & 63;
     const size_t rows = (size_t)g.ntile * 128;
     const float f = pow2f(pw.sh - pw.sp), md = -pow2f(-(pw.edo + pw.ev)) * f, fsp = (float)pw.sp;
     c2 *= pow2f(pw.eq + pw.ek);
@@ -566,7 +566,7 @@ __device__ __forceinline__ void map_row(uint32_t (&s)[32], float nl, float c2, i
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDiffThreads, 1)
 k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
              const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DiffGeom g,
              const __nv_bfloat16* __restrict__ lam, const DiffTile* __restrict__ tiles, const int* __restrict__ seq,
@@ -586,7 +586,7 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
   bwd_setup(bars, warp);
   const uint32_t tbase = bars->tmem_base;
   volatile Abort* ab = &bars->abort;
-
+  if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0) bwd_produce<D>(sm, bars, &tq, &tdo, tl.z + tl.w * 128, h, &tk, &tv, tl.z, n, hk, n, ab, err);
   } else if (warp == 1) {
@@ -632,9 +632,10 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
       }
     }
     is.finish(ok);
-  } else {
+  } else if (warp >= 4) {
+    regs_take();
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - 4) >> 2;
     const int r = quarter * 32 + lane;
     const uint32_t la = (uint32_t)(quarter * 32) << 16;
     const uint32_t cX = tbase + la + 64 * half;
@@ -839,7 +840,10 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
       !make_tmap_16(&tv, b.vs, D, rows, g.Hk, true, 128) || !make_tmap_16(&tdo, b.dos, D, rows, g.H, true, 128))
     return cudaErrorInvalidValue;
   const int smem = BwdLayout<D>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(k_diff_dkdv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = diff_regs_ok(k_diff_dkdv_tc<D>);
+  if (e != cudaSuccess) return e;
+  if ((e = diff_regs_ok(k_diff_dq_tc<D>)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_diff_dkdv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(k_diff_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -851,10 +855,10 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   k_diff_pack_do<true, D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta, b.part, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_dkdv_tc<D><<<g.ntile * g.Hk, kThreads, smem, s>>>(tk, tv, tq, tdo, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
+  k_diff_dkdv_tc<D><<<g.ntile * g.Hk, kDiffThreads, smem, s>>>(tk, tv, tq, tdo, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
                                                            b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_dq_tc<D><<<g.ntile * g.H, kThreads, smem, s>>>(tq, tdo, tk, tv, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
+  k_diff_dq_tc<D><<<g.ntile * g.H, kDiffThreads, smem, s>>>(tq, tdo, tk, tv, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
                                                         b.delta, (__nv_bfloat16*)dq, c2, scale, err);
   count_launch(4);
   return cudaGetLastError();
