@@ -40,11 +40,6 @@ struct NormArgs {
   float eps, inv_d;
 };
 
-template <typename T> __device__ __forceinline__ float ld_f32(const T* p);
-template <> __device__ __forceinline__ float ld_f32<float>(const float* p) { return __ldg(p); }
-template <> __device__ __forceinline__ float ld_f32<__nv_bfloat16>(const __nv_bfloat16* p) {
-  return __bfloat162float(*p);
-}
 __device__ __forceinline__ void st_f32(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -54,24 +49,49 @@ template <bool VEC>
 __device__ __forceinline__ int col_of(int v, int i, int t, int gs) {
   return VEC ? (v * gs + t) * 8 + i : (v * 8 + i) * gs + t;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_cols(const T* row, int v, int t, int gs, int d, float (&x)[8]) {
-  if (VEC) {
+// As they come from memory (a row that is on its way takes no more registers
+// than its bytes), and widened.
+template <typename T, bool VEC> struct Cols;
+template <> struct Cols<__nv_bfloat16, true> {
+  uint4 r;
+  __device__ void load(const __nv_bfloat16* row, int v, int t, int gs, int d) {
     const int c = (v * gs + t) * 8;
+    r = c < d ? __ldg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ float get(int i) const {
+    const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+template <> struct Cols<float, true> {
+  float4 a, b;
+  __device__ void load(const float* row, int v, int t, int gs, int d) {
+    const int c = (v * gs + t) * 8;
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < d) {
-      Vec8<T>::load_f32(row + c, x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      a = __ldg(reinterpret_cast<const float4*>(row + c));
+      b = __ldg(reinterpret_cast<const float4*>(row + c) + 1);
     }
-  } else {
+  }
+  __device__ float get(int i) const {
+    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  }
+};
+template <typename T> struct Cols<T, false> {
+  T x[8];
+  __device__ void load(const T* row, int v, int t, int gs, int d) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = col_of<false>(v, i, t, gs);
-      x[i] = c < d ? ld_f32(row + c) : 0.f;
+      if (c < d) x[i] = row[c];
+      else st_f32(&x[i], 0.f);
     }
   }
-}
+  __device__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return x[i];
+    else return __bfloat162float(x[i]);
+  }
+};
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_cols(T* row, int v, int t, int gs, int d, const float (&x)[8]) {
   if (VEC) {
@@ -93,9 +113,15 @@ __device__ __forceinline__ void load_w(const void* w, int bf16, float none, int 
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = none;
   } else if (bf16) {
-    load_cols<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), v, t, gs, d, x);
+    Cols<__nv_bfloat16, VEC> c;
+    c.load(static_cast<const __nv_bfloat16*>(w), v, t, gs, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = c.get(i);
   } else {
-    load_cols<float, VEC>(static_cast<const float*>(w), v, t, gs, d, x);
+    Cols<float, VEC> c;
+    c.load(static_cast<const float*>(w), v, t, gs, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = c.get(i);
   }
 }
 
@@ -141,26 +167,36 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormA
     load_w<VEC>(a.b, a.wbf16, 0.f, v, t, gs, a.d, b[v]);
   }
   // the block's rows: `base` is the same for the whole block, so every thread
-  // takes part in every reduction
+  // takes part in every reduction. The next R rows are asked for before these
+  // are worked on.
   const long long step = (long long)gridDim.x * groups;
-  for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R) {
-    float xv[R][NV][8], s[R];
+  Cols<T, VEC> nx[R][NV];
+  auto fetch = [&](long long base) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long m = base + r * step + grp;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) load_cols<T, VEC>(x + (m < a.M ? m : 0) * a.ldx, v, t, gs, m < a.M ? a.d : 0, xv[r][v]);
+      for (int v = 0; v < NV; ++v) nx[r][v].load(x + (m < a.M ? m : 0) * a.ldx, v, t, gs, m < a.M ? a.d : 0);
     }
+  };
+  fetch((long long)blockIdx.x * groups);
+  for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R) {
+    Cols<T, VEC> xr[R][NV];
+    float s[R], mu[R], q[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) xr[r][v] = nx[r][v];
+    if (base + step * R < a.M) fetch(base + step * R);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[r] = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[r] += xv[r][v][i];
+        for (int i = 0; i < 8; ++i) s[r] += xr[r][v].get(i);
     }
     group_sum<G, R>(s, red);
-    float mu[R], q[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mu[r] = s[r] * a.inv_d;
@@ -169,8 +205,7 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormA
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float c = col_of<VEC>(v, i, t, gs) < a.d ? xv[r][v][i] - mu[r] : 0.f;
-          xv[r][v][i] = c;
+          const float c = col_of<VEC>(v, i, t, gs) < a.d ? xr[r][v].get(i) - mu[r] : 0.f;
           q[r] = fmaf(c, c, q[r]);
         }
     }
@@ -184,7 +219,7 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormA
         for (int v = 0; v < NV; ++v) {
           float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fmaf(xv[r][v][i] * rs, w[v][i], b[v][i]);
+          for (int i = 0; i < 8; ++i) o[i] = fmaf((xr[r][v].get(i) - mu[r]) * rs, w[v][i], b[v][i]);
           store_cols<T, VEC>(y + m * a.ldy, v, t, gs, a.d, o);
         }
         if (t == 0) {
@@ -206,7 +241,13 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   T* dx = static_cast<T*>(a.dx);
-  float dw[ACC ? NV : 1][8], db[ACC ? NV : 1][8];
+  // w in registers for rows of one vector per thread; reloaded from L1 for longer ones
+  constexpr int WREG = NV == 1 ? 1 : 0;
+  float w[WREG ? NV : 1][8], dw[ACC ? NV : 1][8], db[ACC ? NV : 1][8];
+  if (WREG) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[WREG ? v : 0]);
+  }
   if (ACC) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -217,46 +258,57 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
     __syncthreads();
   }
   const long long step = (long long)gridDim.x * groups;
-  int flip = 0;
-  for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R, flip ^= 1) {
-    float xv[R][NV][8], gv[R][NV][8], mu[R], rs[R], s[2 * R];
+  Cols<T, VEC> nx[R][NV], ny[R][NV];
+  float nmu[R], nrs[R];
+  auto fetch = [&](long long base) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long m = base + r * step + grp, mm = m < a.M ? m : 0;
       const int d = m < a.M ? a.d : 0;
-      mu[r] = m < a.M ? __ldg(a.mean + mm) : 0.f;
-      rs[r] = m < a.M ? __ldg(a.rstd + mm) : 0.f;
+      nmu[r] = m < a.M ? __ldg(a.mean + mm) : 0.f;
+      nrs[r] = m < a.M ? __ldg(a.rstd + mm) : 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        load_cols<T, VEC>(x + mm * a.ldx, v, t, gs, d, xv[r][v]);
-        load_cols<T, VEC>(dy + mm * a.ldy, v, t, gs, d, gv[r][v]);
+        nx[r][v].load(x + mm * a.ldx, v, t, gs, d);
+        ny[r][v].load(dy + mm * a.ldy, v, t, gs, d);
       }
     }
+  };
+  fetch((long long)blockIdx.x * groups);
+  int flip = 0;
+  for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R, flip ^= 1) {
+    Cols<T, VEC> xr[R][NV], yr[R][NV];
+    float mu[R], rs[R], s[2 * R];
 #pragma unroll
-    for (int r = 0; r < 2 * R; ++r) s[r] = 0.f;
+    for (int r = 0; r < R; ++r) {
+      mu[r] = nmu[r];
+      rs[r] = nrs[r];
+      s[2 * r] = s[2 * r + 1] = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        xr[r][v] = nx[r][v];
+        yr[r][v] = ny[r][v];
+      }
+    }
+    if (base + step * R < a.M) fetch(base + step * R);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float w[8];
-      load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w);
+      if (WREG == 0) load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[0]);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool in = col_of<VEC>(v, i, t, gs) < a.d;
-          const float z = in ? (xv[r][v][i] - mu[r]) * rs[r] : 0.f, g = gv[r][v][i];
-          if (a.part) {
-            if (ACC) {
-              dw[ACC ? v : 0][i] = fmaf(g, z, dw[ACC ? v : 0][i]);
-              db[ACC ? v : 0][i] += g;
-            } else if (in) {
-              const int c = col_of<VEC>(v, i, t, gs);
-              dyn[c] = fmaf(g, z, dyn[c]);
-              dyn[a.d + c] += g;
-            }
+          const float z = in ? (xr[r][v].get(i) - mu[r]) * rs[r] : 0.f, g = yr[r][v].get(i);
+          if (ACC) {
+            dw[ACC ? v : 0][i] = fmaf(g, z, dw[ACC ? v : 0][i]);
+            db[ACC ? v : 0][i] += g;
+          } else if (in) {
+            const int c = col_of<VEC>(v, i, t, gs);
+            dyn[c] = fmaf(g, z, dyn[c]);
+            dyn[a.d + c] += g;
           }
-          const float gw = g * w[i];
-          xv[r][v][i] = z;
-          gv[r][v][i] = gw;
+          const float gw = g * w[WREG ? v : 0][i];
           s[2 * r] += gw;
           s[2 * r + 1] = fmaf(gw, z, s[2 * r + 1]);
         }
@@ -264,15 +316,19 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
     }
     group_sum<G, 2 * R>(s, red + (G ? 0 : flip * 64 * R));
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long m = base + r * step + grp;
-      if (m < a.M) {
-        const float c1 = s[2 * r] * a.inv_d, c2 = s[2 * r + 1] * a.inv_d;
+    for (int v = 0; v < NV; ++v) {
+      if (WREG == 0) load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[0]);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
+      for (int r = 0; r < R; ++r) {
+        const long long m = base + r * step + grp;
+        if (m < a.M) {
+          const float c1 = s[2 * r] * a.inv_d, c2 = s[2 * r + 1] * a.inv_d;
           float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = rs[r] * ((gv[r][v][i] - c1) - xv[r][v][i] * c2);
+          for (int i = 0; i < 8; ++i) {
+            const float z = (xr[r][v].get(i) - mu[r]) * rs[r], gw = yr[r][v].get(i) * w[WREG ? v : 0][i];
+            o[i] = rs[r] * ((gw - c1) - z * c2);
+          }
           store_cols<T, VEC>(dx + m * a.ldx, v, t, gs, a.d, o);
         }
       }

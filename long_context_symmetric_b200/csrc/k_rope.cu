@@ -8,20 +8,20 @@
 // a million keeps every digit of the angle that its cosine needs; cosine, sine
 // and the rotation itself are fp32, rounded once on the way out.
 //
-// Bound by HBM: q and k are read once and written once. A block takes kTok
-// tokens: its threads first issue the loads of the first batch of rows, then
-// form the tokens' cosines and sines (one per pair, shared by all heads) in
-// shared memory while those are under way, then rotate and store. W elements
-// to a load: 16 bytes for bf16 when the rows allow it (W = 8), down to single
-// elements for row lengths, strides or rotated widths of odd size.
+// Bound by HBM: q and k are read once and written once. A block takes a few
+// tokens (kTok, or more where a token has few rows): its threads first issue the
+// loads of their first items, then form the tokens' cosines and sines (one per
+// pair, shared by all heads) in shared memory while those are under way, then
+// rotate and store. W elements to a load: 16 bytes when the rows allow it, down
+// to single elements for row lengths, strides or rotated widths of odd size.
 #include "lh_common.cuh"
 
 namespace lh {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kTok = 4;               // tokens per block
-constexpr int kBatch = 4;             // items in flight per thread
+constexpr int kTok = 4;               // tokens per thread, all in flight at once
+constexpr int kRopeSmem = 16384;      // cosines and sines of a block's tokens, at most (or of kTok tokens)
 
 struct RopeArgs {
   const void *q, *k;
@@ -29,20 +29,22 @@ struct RopeArgs {
   const void* pos;
   const double* freq;
   const int* axis;
-  long long tokens;                   // B * N
-  int N, H, Hk, D, R, axes;           // R = rot / 2 pairs
+  int B, N, H, Hk, D, R, axes;        // R = rot / 2 pairs
+  int per_row, rot_items, rows;       // items of a row, those of its rotated part, rows of a token
+  int lanes;                          // groups of kTok tokens to a block
+  unsigned long long m_row, m_tok;    // 2^36 / per_row, 2^36 / (rows per_row), rounded up
   long long q_ld, q_bs, k_ld, k_bs, qo_ld, qo_bs, ko_ld, ko_bs, pos_as, pos_bs;
-  int next, pos64, inverse, tail;     // tail: copy the elements behind the rotated ones
+  int next, pos64, inverse;
   int* err;
 };
+// x / d by the rounded reciprocal m = ceil(2^36 / d): exact while x d < 2^36
+__device__ __forceinline__ int div36(int x, unsigned long long m) { return (int)(((unsigned long long)x * m) >> 36); }
 
 template <typename T, int W> struct Pack;
 template <> struct Pack<__nv_bfloat16, 8> { using V = uint4; };
 template <> struct Pack<__nv_bfloat16, 4> { using V = uint2; };
 template <> struct Pack<__nv_bfloat16, 2> { using V = uint32_t; };
 template <> struct Pack<__nv_bfloat16, 1> { using V = uint16_t; };
-struct alignas(16) F8 { float4 a, b; };
-template <> struct Pack<float, 8> { using V = F8; };
 template <> struct Pack<float, 4> { using V = float4; };
 template <> struct Pack<float, 2> { using V = float2; };
 template <> struct Pack<float, 1> { using V = float; };
@@ -59,138 +61,113 @@ union Chunk {
   __device__ Chunk() {}
 };
 
-// One item: 2 W elements of one row: W pairs (the two halves' vectors, or two
-// neighbouring vectors), or two vectors of the tail.
-struct Item {
-  const char* src;
-  char* dst;
-  int o0, o1;        // element offsets of the two vectors (o1 < 0: none)
-  int pair;          // first pair, or -1: copied as it is
-  int tok;           // token within the block
-};
-
+// An item is 2 W elements of one row: W pairs (the two halves' vectors, or two
+// neighbouring vectors), or two vectors of the tail. A thread takes one item of
+// kTok neighbouring tokens: the addresses are formed once for all of them.
 template <typename T, int W>
-__device__ __forceinline__ bool make_item(const RopeArgs& a, long long tok0, int n, int per_row, int rot_items, int rows, int x,
-                                          Item& it) {
-  if (x >= n) return false;
-  const int row = x / per_row, c = x - row * per_row;
-  it.tok = row / rows;
-  const int h = row - it.tok * rows;
-  const long long g = tok0 + it.tok, b = g / a.N, t = g - b * a.N;
-  const bool isq = h < a.H;
-  it.src = static_cast<const char*>(isq ? a.q : a.k) +
-           sizeof(T) * (isq ? b * a.q_bs + t * a.q_ld + (long long)h * a.D : b * a.k_bs + t * a.k_ld + (long long)(h - a.H) * a.D);
-  it.dst = static_cast<char*>(isq ? a.qo : a.ko) +
-           sizeof(T) * (isq ? b * a.qo_bs + t * a.qo_ld + (long long)h * a.D : b * a.ko_bs + t * a.ko_ld + (long long)(h - a.H) * a.D);
-  if (c < rot_items) {
-    it.pair = c * W;
-    it.o0 = a.next ? 2 * it.pair : it.pair;
-    it.o1 = a.next ? it.o0 + W : it.pair + a.R;
-  } else {
-    it.pair = -1;
-    it.o0 = 2 * a.R + (c - rot_items) * 2 * W;
-    it.o1 = it.o0 + W < a.D ? it.o0 + W : -1;
-  }
-  return true;
-}
-
-template <typename T, int W>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a) {
-  extern __shared__ float2 cs[];                       // [kTok][R]: cosine, sine
+__global__ void __launch_bounds__(kRopeThreads, 3) k_rope(const RopeArgs a) {
+  extern __shared__ float2 cs[];                       // [tokens][R]: cosine, sine
   using V = typename Pack<T, W>::V;
-  const long long tok0 = (long long)blockIdx.x * kTok;
-  const int nt = (int)min((long long)kTok, a.tokens - tok0);
-  const int rot_items = a.R / W, tail_items = a.tail ? (a.D - 2 * a.R + 2 * W - 1) / (2 * W) : 0;
-  const int per_row = rot_items + tail_items, rows = a.H + a.Hk, n = nt * rows * per_row;
+  const int b = blockIdx.y + blockIdx.z * 65535;
+  if (b >= a.B) return;
+  const int t0 = blockIdx.x * a.lanes * kTok, items = a.rows * a.per_row;
+  const int nt = min(a.lanes * kTok, a.N - t0);
   bool ready = false;
-  for (int x0 = threadIdx.x; x0 < n || !ready; x0 += kRopeThreads * kBatch) {
-    Chunk<T, W> u[kBatch], w[kBatch];
-    Item it[kBatch];
-    bool in[kBatch];
+  for (int x = threadIdx.x; x < items * a.lanes || !ready; x += kRopeThreads) {
+    const int grp = a.lanes > 1 ? div36(x, a.m_tok) : 0,      // more than one only below 256 items
+               y = x - grp * items, row = div36(y, a.m_row), c = y - row * a.per_row;
+    const int tk = grp * kTok, live = x < items * a.lanes ? min(kTok, nt - tk) : 0;
+    const bool isq = row < a.H;
+    const int h = isq ? row : row - a.H;
+    const long long ld = isq ? a.q_ld : a.k_ld, lo = isq ? a.qo_ld : a.ko_ld;
+    const bool turn = c < a.rot_items;
+    const int pair = c * W;
+    const int o0 = turn ? (a.next ? 2 * pair : pair) : 2 * a.R + (c - a.rot_items) * 2 * W;
+    const int o1 = turn && !a.next ? pair + a.R : o0 + W;
+    const bool two = o1 < a.D;                          // a tail may end with one vector
+    const T* src = static_cast<const T*>(isq ? a.q : a.k) + (isq ? b * a.q_bs : b * a.k_bs) + (t0 + tk) * ld + h * a.D;
+    T* dst = static_cast<T*>(isq ? a.qo : a.ko) + (isq ? b * a.qo_bs : b * a.ko_bs) + (t0 + tk) * lo + h * a.D;
+    Chunk<T, W> u[kTok], w[kTok];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      in[k] = make_item<T, W>(a, tok0, n, per_row, rot_items, rows, x0 + k * kRopeThreads, it[k]);
-      if (in[k]) {
-        const T* s = reinterpret_cast<const T*>(it[k].src);
-        u[k].v = *reinterpret_cast<const V*>(s + it[k].o0);
-        if (it[k].o1 >= 0) w[k].v = *reinterpret_cast<const V*>(s + it[k].o1);
+    for (int k = 0; k < kTok; ++k) {
+      if (k < live) {
+        u[k].v = *reinterpret_cast<const V*>(src + k * ld + o0);
+        if (two) w[k].v = *reinterpret_cast<const V*>(src + k * ld + o1);
       }
     }
     if (!ready) {
-      for (int y = threadIdx.x; y < nt * a.R; y += kRopeThreads) {
-        const int tk = y / a.R, i = y - tk * a.R;
-        const long long g = tok0 + tk, b = g / a.N, t = g - b * a.N;
+      for (int z = threadIdx.x; z < nt * a.R; z += kRopeThreads) {
+        const int tok = z / a.R, i = z - tok * a.R;
         int ax = __ldg(a.axis + i);
         if (ax < 0 || ax >= a.axes) {
           report_error(a.err, LH_ERR_DEVICE, 401);
           ax = 0;
         }
-        const long long at = b * a.pos_bs + ax * a.pos_as + t;
+        const long long at = b * a.pos_bs + ax * a.pos_as + t0 + tok;
         const double p = a.pos64 ? (double)static_cast<const long long*>(a.pos)[at] : (double)static_cast<const int*>(a.pos)[at];
         // quarter turns: 4 angle / (2 pi) = q + r, |r| <= 1/2
         const double turns = p * (__ldg(a.freq + i) * 0.63661977236758134308);
         const double qd = rint(turns);
-        float s, c;
-        sincospif((float)((turns - qd) * 0.5), &s, &c);
+        float s, co;
+        sincospif((float)((turns - qd) * 0.5), &s, &co);
         const int q4 = (int)((long long)qd & 3);
-        const float cc = (q4 & 1) ? s : c, ss = (q4 & 1) ? c : s;
-        const float co = (q4 == 1 || q4 == 2) ? -cc : cc, si = q4 >= 2 ? -ss : ss;
-        cs[y] = make_float2(co, a.inverse ? -si : si);
+        const float cc = (q4 & 1) ? s : co, ss = (q4 & 1) ? co : s;
+        const float rc = (q4 == 1 || q4 == 2) ? -cc : cc, rs = q4 >= 2 ? -ss : ss;
+        cs[z] = make_float2(rc, a.inverse ? -rs : rs);
       }
       __syncthreads();
       ready = true;
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (!in[k]) continue;
-      T* d = reinterpret_cast<T*>(it[k].dst);
-      if (it[k].pair >= 0) {
-        const float2* c = cs + it[k].tok * a.R + it[k].pair;
+    for (int k = 0; k < kTok; ++k) {
+      if (k >= live) break;
+      if (turn) {
+        const float2* p = cs + (tk + k) * a.R + pair;
         if (a.next && W > 1) {
           // pairs of neighbours: elements (0, 1), (2, 3) .. of u, then of w
 #pragma unroll
           for (int e = 0; e < W; e += 2) {
-            const float2 c0 = c[e / 2], c1 = c[(W + e) / 2];
-            const float x0_ = to_f(u[k].e[e]), y0_ = to_f(u[k].e[e + (W > 1)]);
-            const float x1_ = to_f(w[k].e[e]), y1_ = to_f(w[k].e[e + (W > 1)]);
-            from_f(x0_ * c0.x - y0_ * c0.y, u[k].e[e]);
-            from_f(y0_ * c0.x + x0_ * c0.y, u[k].e[e + (W > 1)]);
-            from_f(x1_ * c1.x - y1_ * c1.y, w[k].e[e]);
-            from_f(y1_ * c1.x + x1_ * c1.y, w[k].e[e + (W > 1)]);
+            const float2 c0 = p[e / 2], c1 = p[(W + e) / 2];
+            const float x0 = to_f(u[k].e[e]), y0 = to_f(u[k].e[e + (W > 1)]);
+            const float x1 = to_f(w[k].e[e]), y1 = to_f(w[k].e[e + (W > 1)]);
+            from_f(x0 * c0.x - y0 * c0.y, u[k].e[e]);
+            from_f(y0 * c0.x + x0 * c0.y, u[k].e[e + (W > 1)]);
+            from_f(x1 * c1.x - y1 * c1.y, w[k].e[e]);
+            from_f(y1 * c1.x + x1 * c1.y, w[k].e[e + (W > 1)]);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            const float2 c0 = c[e];
             const float xa = to_f(u[k].e[e]), xb = to_f(w[k].e[e]);
-            from_f(xa * c0.x - xb * c0.y, u[k].e[e]);
-            from_f(xb * c0.x + xa * c0.y, w[k].e[e]);
+            from_f(xa * p[e].x - xb * p[e].y, u[k].e[e]);
+            from_f(xb * p[e].x + xa * p[e].y, w[k].e[e]);
           }
         }
       }
-      *reinterpret_cast<V*>(d + it[k].o0) = u[k].v;
-      if (it[k].o1 >= 0) *reinterpret_cast<V*>(d + it[k].o1) = w[k].v;
+      *reinterpret_cast<V*>(dst + k * lo + o0) = u[k].v;
+      if (two) *reinterpret_cast<V*>(dst + k * lo + o1) = w[k].v;
     }
   }
 }
 
 template <typename T, int W>
-cudaError_t rope_t(const RopeArgs& a, cudaStream_t st) {
-  const long long blocks = (a.tokens + kTok - 1) / kTok;
-  const size_t sm = (size_t)kTok * a.R * sizeof(float2);
-  k_rope<T, W><<<(unsigned)blocks, kRopeThreads, sm, st>>>(a);
+cudaError_t rope_t(RopeArgs a, int tail, cudaStream_t st) {
+  a.rot_items = a.R / W;
+  a.per_row = a.rot_items + (tail + 2 * W - 1) / (2 * W);
+  a.rows = a.H + a.Hk;
+  const int items = a.rows * a.per_row;
+  a.lanes = kRopeThreads / items;
+  const int fit = kRopeSmem / (kTok * a.R * (int)sizeof(float2));
+  if (a.lanes > fit) a.lanes = fit;
+  if (a.lanes > (a.N + kTok - 1) / kTok) a.lanes = (a.N + kTok - 1) / kTok;
+  if (a.lanes < 1) a.lanes = 1;
+  a.m_row = ((1ull << 36) + a.per_row - 1) / a.per_row;
+  a.m_tok = ((1ull << 36) + items - 1) / items;
+  const int toks = a.lanes * kTok;
+  const dim3 grid((a.N + toks - 1) / toks, a.B < 65535 ? a.B : 65535, (a.B + 65534) / 65535);
+  k_rope<T, W><<<grid, kRopeThreads, (size_t)toks * a.R * sizeof(float2), st>>>(a);
   count_launch();
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t rope_w(const RopeArgs& a, int w, cudaStream_t st) {
-  switch (w) {
-    case 8: return rope_t<T, 8>(a, st);
-    case 4: return rope_t<T, 4>(a, st);
-    case 2: return rope_t<T, 2>(a, st);
-    default: return rope_t<T, 1>(a, st);
-  }
 }
 
 }  // namespace
@@ -199,9 +176,8 @@ cudaError_t launch_rope(const lh_rope_config& c, const void* q, const void* k, c
                         const int32_t* axis, int inverse, void* qo, void* ko, int* err, cudaStream_t st) {
   RopeArgs a{};
   a.q = q; a.k = k; a.qo = qo; a.ko = ko; a.pos = pos; a.freq = freq; a.axis = axis; a.err = err;
-  a.tokens = (long long)c.B * c.N;
-  if (a.tokens == 0) return cudaSuccess;
-  a.N = c.N; a.H = c.H; a.Hk = c.Hk; a.D = c.D; a.R = c.rot / 2; a.axes = c.axes;
+  if (c.B == 0 || c.N == 0) return cudaSuccess;
+  a.B = c.B; a.N = c.N; a.H = c.H; a.Hk = c.Hk; a.D = c.D; a.R = c.rot / 2; a.axes = c.axes;
   const long long wq = (long long)c.H * c.D, wk = (long long)c.Hk * c.D;
   a.q_ld = c.q_ld ? c.q_ld : wq; a.qo_ld = c.qo_ld ? c.qo_ld : wq;
   a.k_ld = c.k_ld ? c.k_ld : wk; a.ko_ld = c.ko_ld ? c.ko_ld : wk;
@@ -210,12 +186,25 @@ cudaError_t launch_rope(const lh_rope_config& c, const void* q, const void* k, c
   a.pos_as = c.pos_as; a.pos_bs = c.pos_bs;
   a.next = c.pairs == LH_ROPE_NEXT; a.pos64 = c.pos64; a.inverse = inverse;
   const bool inplace = q == qo && k == ko && a.q_ld == a.qo_ld && a.q_bs == a.qo_bs && (!c.Hk || (a.k_ld == a.ko_ld && a.k_bs == a.ko_bs));
-  a.tail = !inplace && c.rot < c.D;
-  // the widest vector that every row start, both halves' starts and the tail's
-  // start are multiples of
+  const int tail = inplace ? 0 : c.D - c.rot;      // elements that are copied
+  // the widest vector, up to 16 bytes, that every row start, both halves' starts
+  // and the tail's start are multiples of
   const long long all = (long long)c.D | a.R | a.q_ld | a.q_bs | a.k_ld | a.k_bs | a.qo_ld | a.qo_bs | a.ko_ld | a.ko_bs;
   const int w = all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
-  return c.dtype == LH_BF16 ? rope_w<__nv_bfloat16>(a, w, st) : rope_w<float>(a, w, st);
+  if (c.dtype == LH_BF16) {
+    switch (w) {
+      case 8: return rope_t<__nv_bfloat16, 8>(a, tail, st);
+      case 4: return rope_t<__nv_bfloat16, 4>(a, tail, st);
+      case 2: return rope_t<__nv_bfloat16, 2>(a, tail, st);
+      default: return rope_t<__nv_bfloat16, 1>(a, tail, st);
+    }
+  }
+  switch (w) {
+    case 8:
+    case 4: return rope_t<float, 4>(a, tail, st);
+    case 2: return rope_t<float, 2>(a, tail, st);
+    default: return rope_t<float, 1>(a, tail, st);
+  }
 }
 
 }  // namespace lh
