@@ -30,6 +30,7 @@ namespace lh {
 namespace {
 
 constexpr int kNormThreads = 512;      // threads that hold one long row at most
+constexpr int kRowThreads = 64, kRowBlocks = 10;   // forward pass of a row per warp
 
 struct NormArgs {
   const void *x, *w, *b, *dy;
@@ -105,6 +106,21 @@ __device__ __forceinline__ void store_cols(T* row, int v, int t, int gs, int d, 
     }
   }
 }
+// Arithmetic goes in pairs (packed fp32 instructions): columns 2 i and 2 i + 1 of
+// a vector.
+template <typename C> __device__ __forceinline__ float2 pair_of(const C& c, int i) {
+  return make_float2(c.get(2 * i), c.get(2 * i + 1));
+}
+__device__ __forceinline__ float2 pair_of(const float (&x)[8], int i) { return make_float2(x[2 * i], x[2 * i + 1]); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// -mean, for columns past d 0 (they were read as 0, so their z is 0): one test
+// per vector of neighbours
+template <bool VEC>
+__device__ __forceinline__ float2 neg_mean(float mu, int v, int i, int t, int gs, int d) {
+  if (VEC) return both((v * gs + t) * 8 < d ? -mu : 0.f);
+  return make_float2(col_of<false>(v, 2 * i, t, gs) < d ? -mu : 0.f, col_of<false>(v, 2 * i + 1, t, gs) < d ? -mu : 0.f);
+}
+
 // weight or bias columns (NULL: the given constant)
 template <bool VEC>
 __device__ __forceinline__ void load_w(const void* w, int bf16, float none, int v, int t, int gs, int d,
@@ -154,21 +170,24 @@ __device__ __forceinline__ void group_sum(float (&v)[n], float* red) {
 }
 
 template <typename T, bool VEC, int G, int NV, int R>
-__global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormArgs a) {
+__global__ void __launch_bounds__(G == 0 ? kNormThreads : NV == 1 ? 256 : kRowThreads, G == 0 ? 1 : NV == 1 ? 0 : kRowBlocks)
+k_norm_fwd(const NormArgs a) {
+  constexpr bool AHEAD = G == 0 || NV == 1;
   __shared__ float red[G ? 1 : 2 * 32 * R];
   const int gs = G ? G : (int)blockDim.x, t = G ? (int)threadIdx.x % G : (int)threadIdx.x;
   const int groups = G ? (int)blockDim.x / G : 1, grp = G ? (int)threadIdx.x / G : 0;
   const T* x = static_cast<const T*>(a.x);
   T* y = static_cast<T*>(a.y);
-  float w[NV][8], b[NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[v]);
-    load_w<VEC>(a.b, a.wbf16, 0.f, v, t, gs, a.d, b[v]);
+  // w and b in registers for rows of one vector per thread; reloaded from L1 for longer ones
+  constexpr bool WREG = NV == 1;
+  float w[8], b[8];
+  if (WREG) {
+    load_w<VEC>(a.w, a.wbf16, 1.f, 0, t, gs, a.d, w);
+    load_w<VEC>(a.b, a.wbf16, 0.f, 0, t, gs, a.d, b);
   }
   // the block's rows: `base` is the same for the whole block, so every thread
-  // takes part in every reduction. The next R rows are asked for before these
-  // are worked on.
+  // takes part in every reduction. AHEAD: the next R rows are asked for before
+  // these are worked on.
   const long long step = (long long)gridDim.x * groups;
   Cols<T, VEC> nx[R][NV];
   auto fetch = [&](long long base) {
@@ -179,35 +198,38 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormA
       for (int v = 0; v < NV; ++v) nx[r][v].load(x + (m < a.M ? m : 0) * a.ldx, v, t, gs, m < a.M ? a.d : 0);
     }
   };
-  fetch((long long)blockIdx.x * groups);
+  if (AHEAD) fetch((long long)blockIdx.x * groups);
   for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R) {
     Cols<T, VEC> xr[R][NV];
     float s[R], mu[R], q[R];
+    if (!AHEAD) fetch(base);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int v = 0; v < NV; ++v) xr[r][v] = nx[r][v];
-    if (base + step * R < a.M) fetch(base + step * R);
+    if (AHEAD && base + step * R < a.M) fetch(base + step * R);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[r] = 0.f;
+      float2 p = both(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[r] += xr[r][v].get(i);
+        for (int i = 0; i < 4; ++i) p = __fadd2_rn(p, pair_of(xr[r][v], i));
+      s[r] = p.x + p.y;
     }
     group_sum<G, R>(s, red);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mu[r] = s[r] * a.inv_d;
-      q[r] = 0.f;
+      float2 p = both(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float c = col_of<VEC>(v, i, t, gs) < a.d ? xr[r][v].get(i) - mu[r] : 0.f;
-          q[r] = fmaf(c, c, q[r]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 c = __fadd2_rn(pair_of(xr[r][v], i), neg_mean<VEC>(mu[r], v, i, t, gs, a.d));
+          p = __ffma2_rn(c, c, p);
         }
+      q[r] = p.x + p.y;
     }
     group_sum<G, R>(q, red + (G ? 0 : 32 * R));
 #pragma unroll
@@ -218,8 +240,17 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormA
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           float o[8];
+          if (!WREG) {
+            load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w);
+            load_w<VEC>(a.b, a.wbf16, 0.f, v, t, gs, a.d, b);
+          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = fmaf((xr[r][v].get(i) - mu[r]) * rs, w[v][i], b[v][i]);
+          for (int i = 0; i < 4; ++i) {
+            const float2 z = __fmul2_rn(__fadd2_rn(pair_of(xr[r][v], i), both(-mu[r])), both(rs));
+            const float2 f = __ffma2_rn(z, pair_of(w, i), pair_of(b, i));
+            o[2 * i] = f.x;
+            o[2 * i + 1] = f.y;
+          }
           store_cols<T, VEC>(y + m * a.ldy, v, t, gs, a.d, o);
         }
         if (t == 0) {
@@ -233,7 +264,7 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_fwd(const NormA
 
 // ACC: dw and db of this thread's columns in registers (false: in shared memory).
 template <typename T, bool VEC, int G, int NV, int R, bool ACC>
-__global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormArgs a) {
+__global__ void __launch_bounds__(G ? 256 : kNormThreads, G ? 2 : 1) k_norm_bwd(const NormArgs a) {
   extern __shared__ float dyn[];
   __shared__ float red[G ? 1 : 2 * 32 * 2 * R];
   const int gs = G ? G : (int)blockDim.x, t = G ? (int)threadIdx.x % G : (int)threadIdx.x;
@@ -243,7 +274,8 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
   T* dx = static_cast<T*>(a.dx);
   // w in registers for rows of one vector per thread; reloaded from L1 for longer ones
   constexpr int WREG = NV == 1 ? 1 : 0;
-  float w[WREG ? NV : 1][8], dw[ACC ? NV : 1][8], db[ACC ? NV : 1][8];
+  float w[WREG ? NV : 1][8];
+  float2 dw[ACC ? NV : 1][4], db[ACC ? NV : 1][4];
   if (WREG) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[WREG ? v : 0]);
@@ -252,7 +284,7 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dw[ACC ? v : 0][i] = db[ACC ? v : 0][i] = 0.f;
+      for (int i = 0; i < 4; ++i) dw[ACC ? v : 0][i] = db[ACC ? v : 0][i] = both(0.f);
   } else {
     for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) dyn[c] = 0.f;
     __syncthreads();
@@ -277,57 +309,71 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
   fetch((long long)blockIdx.x * groups);
   int flip = 0;
   for (long long base = (long long)blockIdx.x * groups; base < a.M; base += step * R, flip ^= 1) {
-    Cols<T, VEC> xr[R][NV], yr[R][NV];
-    float mu[R], rs[R], s[2 * R];
+    float2 zv[R][NV][4], gv[R][NV][4];
+    float rs[R], s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      mu[r] = nmu[r];
       rs[r] = nrs[r];
-      s[2 * r] = s[2 * r + 1] = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        xr[r][v] = nx[r][v];
-        yr[r][v] = ny[r][v];
-      }
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          zv[r][v][i] = __fmul2_rn(__fadd2_rn(pair_of(nx[r][v], i), neg_mean<VEC>(nmu[r], v, i, t, gs, a.d)), both(nrs[r]));
+          gv[r][v][i] = pair_of(ny[r][v], i);
+        }
     }
     if (base + step * R < a.M) fetch(base + step * R);
+    float2 s1[R], s2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s1[r] = s2[r] = both(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (WREG == 0) load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[0]);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool in = col_of<VEC>(v, i, t, gs) < a.d;
-          const float z = in ? (xr[r][v].get(i) - mu[r]) * rs[r] : 0.f, g = yr[r][v].get(i);
+        for (int i = 0; i < 4; ++i) {
+          const float2 z = zv[r][v][i], g = gv[r][v][i];
           if (ACC) {
-            dw[ACC ? v : 0][i] = fmaf(g, z, dw[ACC ? v : 0][i]);
-            db[ACC ? v : 0][i] += g;
-          } else if (in) {
-            const int c = col_of<VEC>(v, i, t, gs);
-            dyn[c] = fmaf(g, z, dyn[c]);
-            dyn[a.d + c] += g;
+            dw[ACC ? v : 0][i] = __ffma2_rn(g, z, dw[ACC ? v : 0][i]);
+            db[ACC ? v : 0][i] = __fadd2_rn(db[ACC ? v : 0][i], g);
+          } else {
+            const int c = col_of<VEC>(v, 2 * i, t, gs), e = col_of<VEC>(v, 2 * i + 1, t, gs);
+            if (c < a.d) {
+              dyn[c] = fmaf(g.x, z.x, dyn[c]);
+              dyn[a.d + c] += g.x;
+            }
+            if (e < a.d) {
+              dyn[e] = fmaf(g.y, z.y, dyn[e]);
+              dyn[a.d + e] += g.y;
+            }
           }
-          const float gw = g * w[WREG ? v : 0][i];
-          s[2 * r] += gw;
-          s[2 * r + 1] = fmaf(gw, z, s[2 * r + 1]);
+          const float2 gw = __fmul2_rn(g, pair_of(w[WREG ? v : 0], i));
+          gv[r][v][i] = gw;
+          s1[r] = __fadd2_rn(s1[r], gw);
+          s2[r] = __ffma2_rn(gw, z, s2[r]);
         }
       }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[2 * r] = s1[r].x + s1[r].y;
+      s[2 * r + 1] = s2[r].x + s2[r].y;
+    }
     group_sum<G, 2 * R>(s, red + (G ? 0 : flip * 64 * R));
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (WREG == 0) load_w<VEC>(a.w, a.wbf16, 1.f, v, t, gs, a.d, w[0]);
+    for (int r = 0; r < R; ++r) {
+      const long long m = base + r * step + grp;
+      if (m < a.M) {
+        const float c1 = s[2 * r] * a.inv_d, c2 = s[2 * r + 1] * a.inv_d;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const long long m = base + r * step + grp;
-        if (m < a.M) {
-          const float c1 = s[2 * r] * a.inv_d, c2 = s[2 * r + 1] * a.inv_d;
+        for (int v = 0; v < NV; ++v) {
           float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float z = (xr[r][v].get(i) - mu[r]) * rs[r], gw = yr[r][v].get(i) * w[WREG ? v : 0][i];
-            o[i] = rs[r] * ((gw - c1) - z * c2);
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __fmul2_rn(both(rs[r]), __ffma2_rn(zv[r][v][i], both(-c2), __fadd2_rn(gv[r][v][i], both(-c1))));
+            o[2 * i] = f.x;
+            o[2 * i + 1] = f.y;
           }
           store_cols<T, VEC>(dx + m * a.ldx, v, t, gs, a.d, o);
         }
@@ -346,8 +392,8 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
       for (int i = 0; i < 8; ++i) {
         const int c = col_of<VEC>(v, i, t, gs);
         if (c < a.d) {
-          out[c] = dw[ACC ? v : 0][i];
-          out[a.d + c] = db[ACC ? v : 0][i];
+          out[c] = i & 1 ? dw[ACC ? v : 0][i / 2].y : dw[ACC ? v : 0][i / 2].x;
+          out[a.d + c] = i & 1 ? db[ACC ? v : 0][i / 2].y : db[ACC ? v : 0][i / 2].x;
         }
       }
   } else {
@@ -358,8 +404,8 @@ __global__ void __launch_bounds__(G ? 256 : kNormThreads) k_norm_bwd(const NormA
       for (int i = 0; i < 8; ++i) {
         const int c = col_of<VEC>(v, i, t, gs);
         if (c < a.d) {
-          dyn[(2 * grp) * a.d + c] = dw[ACC ? v : 0][i];
-          dyn[(2 * grp + 1) * a.d + c] = db[ACC ? v : 0][i];
+          dyn[(2 * grp) * a.d + c] = i & 1 ? dw[ACC ? v : 0][i / 2].y : dw[ACC ? v : 0][i / 2].x;
+          dyn[(2 * grp + 1) * a.d + c] = i & 1 ? db[ACC ? v : 0][i / 2].y : db[ACC ? v : 0][i / 2].x;
         }
       }
     __syncthreads();
@@ -380,6 +426,7 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ 
   float s = 0.f;
   if (c < 2 * d) {
     const float* p = part + c;
+#pragma unroll 4
     for (int k = threadIdx.y; k < nb; k += 32) s += __ldg(p + (size_t)k * 2 * d);
   }
   sm[threadIdx.y][threadIdx.x] = s;
@@ -403,8 +450,9 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* __restrict__ 
 struct NormShape {
   int G, threads, nv;
 };
-NormShape norm_shape(int d) {
+NormShape norm_shape(int d, bool warp_rows) {
   const int nvec = (d + 7) / 8;
+  if (warp_rows && nvec > 32 && nvec <= 256) return {32, 256, nvec <= 64 ? 2 : nvec <= 128 ? 4 : 8};
   if (nvec <= 32) {
     int G = 4;
     while (G < nvec) G *= 2;
@@ -420,45 +468,62 @@ int norm_blocks(const NormShape& s, long long M, int R) {
   const long long most = (long long)kNormSMs * (1024 / s.threads < 1 ? 1 : 1024 / s.threads);
   return (int)(need < most ? need : most);
 }
-constexpr int kRF = 2, kRB = 2;      // rows in flight per group, forward and backward (nv = 1)
+constexpr int kRF = 2;               // rows in flight per group, forward pass (nv = 1)
 
 template <typename T, bool VEC>
 cudaError_t fwd_t(const NormShape& s, const NormArgs& a, cudaStream_t st) {
-  const int nb = norm_blocks(s, a.M, s.nv == 1 ? kRF : 1);
-  switch (s.G) {
-    case 4: k_norm_fwd<T, VEC, 4, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
-    case 8: k_norm_fwd<T, VEC, 8, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
-    case 16: k_norm_fwd<T, VEC, 16, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
-    case 32: k_norm_fwd<T, VEC, 32, 1, kRF><<<nb, s.threads, 0, st>>>(a); break;
-    default:
-      if (s.nv == 1) k_norm_fwd<T, VEC, 0, 1, kRF><<<nb, s.threads, 0, st>>>(a);
-      else if (s.nv == 2) k_norm_fwd<T, VEC, 0, 2, 1><<<nb, s.threads, 0, st>>>(a);
-      else k_norm_fwd<T, VEC, 0, 4, 1><<<nb, s.threads, 0, st>>>(a);
+  if (s.G == 32 && s.nv > 1) {
+    // a warp per row, every row in flight at once
+    if constexpr (VEC && sizeof(T) == 2) {
+      const int R = s.nv == 2 ? 2 : 1;
+      const long long rows = kRowThreads / 32 * R, need = (a.M + rows - 1) / rows;
+      const unsigned nb = (unsigned)(need < 0x7fffffff ? need : 0x7fffffff);
+      auto kern = s.nv == 2 ? k_norm_fwd<T, VEC, 32, 2, 2> : s.nv == 4 ? k_norm_fwd<T, VEC, 32, 4, 1> : k_norm_fwd<T, VEC, 32, 8, 1>;
+      kern<<<nb, kRowThreads, 0, st>>>(a);
+    }
+  } else {
+    const int nb = norm_blocks(s, a.M, s.nv == 1 ? kRF : 1);
+    auto kern = s.G == 4    ? k_norm_fwd<T, VEC, 4, 1, kRF>
+                : s.G == 8  ? k_norm_fwd<T, VEC, 8, 1, kRF>
+                : s.G == 16 ? k_norm_fwd<T, VEC, 16, 1, kRF>
+                : s.G == 32 ? k_norm_fwd<T, VEC, 32, 1, kRF>
+                : s.nv == 1 ? k_norm_fwd<T, VEC, 0, 1, kRF>
+                : s.nv == 2 ? k_norm_fwd<T, VEC, 0, 2, 1>
+                            : k_norm_fwd<T, VEC, 0, 4, 1>;
+    kern<<<nb, s.threads, 0, st>>>(a);
   }
   count_launch();
   return cudaGetLastError();
 }
 
+// Rows in flight of the backward kernel (one vector per thread): what the
+// registers hold without spilling. 1M rows of 128 bf16: 147 us with 2, 130 with 3;
+// 98,304 of 2,048: 282, 224, 265 with 1, 2, 3; 5,003 odd fp32 rows of 1,537: 34, 41
+// with 1, 2.
+template <typename T, bool VEC> constexpr int bwd_rows(int G) {
+  return !VEC ? 1 : G > 0 && sizeof(T) == 2 ? 3 : 2;
+}
+int bwd_blocks(const NormShape& s, long long M, bool vec, bool bf16) {
+  const int R = s.nv > 1 ? 1 : !vec ? 1 : s.G > 0 && bf16 ? 3 : 2;
+  return norm_blocks(s, M, R);
+}
+
 template <typename T, bool VEC>
 cudaError_t bwd_t(const NormShape& s, const NormArgs& a, int nb, cudaStream_t st) {
+  constexpr int RG = bwd_rows<T, VEC>(32), RB = bwd_rows<T, VEC>(0);
   const size_t sm = s.G ? (size_t)(s.threads / s.G) * 2 * a.d * 4 : s.nv == 4 ? (size_t)2 * a.d * 4 : 0;
-  switch (s.G) {
-    case 4: k_norm_bwd<T, VEC, 4, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
-    case 8: k_norm_bwd<T, VEC, 8, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
-    case 16: k_norm_bwd<T, VEC, 16, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
-    case 32: k_norm_bwd<T, VEC, 32, 1, kRB, true><<<nb, s.threads, sm, st>>>(a); break;
-    default:
-      if (s.nv == 1) {
-        k_norm_bwd<T, VEC, 0, 1, kRB, true><<<nb, s.threads, sm, st>>>(a);
-      } else if (s.nv == 2) {
-        k_norm_bwd<T, VEC, 0, 2, 1, true><<<nb, s.threads, sm, st>>>(a);
-      } else {
-        auto kern = k_norm_bwd<T, VEC, 0, 4, 1, false>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-        if (e != cudaSuccess) return e;
-        kern<<<nb, s.threads, sm, st>>>(a);
-      }
+  auto kern = s.G == 4    ? k_norm_bwd<T, VEC, 4, 1, RG, true>
+              : s.G == 8  ? k_norm_bwd<T, VEC, 8, 1, RG, true>
+              : s.G == 16 ? k_norm_bwd<T, VEC, 16, 1, RG, true>
+              : s.G == 32 ? k_norm_bwd<T, VEC, 32, 1, RG, true>
+              : s.nv == 1 ? k_norm_bwd<T, VEC, 0, 1, RB, true>
+              : s.nv == 2 ? k_norm_bwd<T, VEC, 0, 2, 1, true>
+                          : k_norm_bwd<T, VEC, 0, 4, 1, false>;
+  if (sm > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
   }
+  kern<<<nb, s.threads, sm, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -471,8 +536,8 @@ bool norm_vec(const lh_norm_config& c, long long ldx, long long ldy) {
 
 // Partial rows of dw and db: one of 2 d floats per block of the backward kernel.
 size_t norm_ws_bytes(const lh_norm_config& c) {
-  const NormShape s = norm_shape(c.d);
-  return (size_t)norm_blocks(s, c.M, s.nv == 1 ? kRB : 1) * 2 * c.d * sizeof(float);
+  const bool vec = norm_vec(c, c.ldx ? c.ldx : c.d, c.ldy ? c.ldy : c.d);
+  return (size_t)bwd_blocks(norm_shape(c.d, false), c.M, vec, c.dtype == LH_BF16) * 2 * c.d * sizeof(float);
 }
 
 cudaError_t launch_norm_fwd(const lh_norm_config& c, const void* x, const void* w, const void* b, void* y,
@@ -482,8 +547,11 @@ cudaError_t launch_norm_fwd(const lh_norm_config& c, const void* x, const void* 
   a.x = x; a.w = w; a.b = b; a.y = y; a.mean = mean; a.rstd = rstd;
   a.M = c.M; a.ldx = c.ldx ? c.ldx : c.d; a.ldy = c.ldy ? c.ldy : c.d; a.d = c.d;
   a.wbf16 = c.wdtype == LH_BF16; a.eps = c.eps; a.inv_d = 1.f / (float)c.d;
-  const NormShape s = norm_shape(c.d);
   const bool vec = norm_vec(c, a.ldx, a.ldy);
+  // a warp per row where there are rows enough to fill the GPU with warps:
+  // 98,304 rows of 2,048: 150 us against 171 with a block per row; 64 rows of
+  // 1,024: 7.2 against 4.8
+  const NormShape s = norm_shape(c.d, vec && c.dtype == LH_BF16 && c.M >= 16 * kNormSMs);
   if (c.dtype == LH_BF16)
     return vec ? fwd_t<__nv_bfloat16, true>(s, a, st) : fwd_t<__nv_bfloat16, false>(s, a, st);
   return vec ? fwd_t<float, true>(s, a, st) : fwd_t<float, false>(s, a, st);
@@ -496,10 +564,10 @@ cudaError_t launch_norm_bwd(const lh_norm_config& c, const void* dy, const void*
   a.part = dw || db ? part : nullptr;
   a.M = c.M; a.ldx = c.ldx ? c.ldx : c.d; a.ldy = c.ldy ? c.ldy : c.d; a.d = c.d;
   a.wbf16 = c.wdtype == LH_BF16; a.eps = c.eps; a.inv_d = 1.f / (float)c.d;
-  const NormShape s = norm_shape(c.d);
-  const int nb = norm_blocks(s, c.M, s.nv == 1 ? kRB : 1);
+  const NormShape s = norm_shape(c.d, false);
+  const bool vec = norm_vec(c, a.ldx, a.ldy);
+  const int nb = bwd_blocks(s, c.M, vec, c.dtype == LH_BF16);
   if (c.M > 0) {
-    const bool vec = norm_vec(c, a.ldx, a.ldy);
     cudaError_t e;
     if (c.dtype == LH_BF16)
       e = vec ? bwd_t<__nv_bfloat16, true>(s, a, nb, st) : bwd_t<__nv_bfloat16, false>(s, a, nb, st);

@@ -19,7 +19,7 @@
 namespace lh {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 64;
 constexpr int kTok = 4;               // tokens per thread, all in flight at once
 constexpr int kRopeSmem = 16384;      // cosines and sines of a block's tokens, at most (or of kTok tokens)
 
@@ -54,6 +54,15 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float v, float& x) { x = v; }
 __device__ __forceinline__ void from_f(float v, __nv_bfloat16& x) { x = __float2bfloat16_rn(v); }
 
+template <bool S, typename V> __device__ __forceinline__ V ld_once(const V* p) {
+  if constexpr (S) return __ldcs(p);
+  else return *p;
+}
+template <bool S, typename V> __device__ __forceinline__ void st_once(V* p, const V& v) {
+  if constexpr (S) __stcs(p, v);
+  else *p = v;
+}
+
 template <typename T, int W>
 union Chunk {
   typename Pack<T, W>::V v;
@@ -64,8 +73,9 @@ union Chunk {
 // An item is 2 W elements of one row: W pairs (the two halves' vectors, or two
 // neighbouring vectors), or two vectors of the tail. A thread takes one item of
 // kTok neighbouring tokens: the addresses are formed once for all of them.
-template <typename T, int W>
-__global__ void __launch_bounds__(kRopeThreads, 3) k_rope(const RopeArgs a) {
+// STREAM: data beyond what L2 holds is marked to leave it first.
+template <typename T, int W, bool STREAM>
+__global__ void __launch_bounds__(kRopeThreads, 12) k_rope(const RopeArgs a) {
   extern __shared__ float2 cs[];                       // [tokens][R]: cosine, sine
   using V = typename Pack<T, W>::V;
   const int b = blockIdx.y + blockIdx.z * 65535;
@@ -91,8 +101,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) k_rope(const RopeArgs a) {
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
       if (k < live) {
-        u[k].v = *reinterpret_cast<const V*>(src + k * ld + o0);
-        if (two) w[k].v = *reinterpret_cast<const V*>(src + k * ld + o1);
+        u[k].v = ld_once<STREAM>(reinterpret_cast<const V*>(src + k * ld + o0));
+        if (two) w[k].v = ld_once<STREAM>(reinterpret_cast<const V*>(src + k * ld + o1));
       }
     }
     if (!ready) {
@@ -144,8 +154,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) k_rope(const RopeArgs a) {
           }
         }
       }
-      *reinterpret_cast<V*>(dst + k * lo + o0) = u[k].v;
-      if (two) *reinterpret_cast<V*>(dst + k * lo + o1) = w[k].v;
+      st_once<STREAM>(reinterpret_cast<V*>(dst + k * lo + o0), u[k].v);
+      if (two) st_once<STREAM>(reinterpret_cast<V*>(dst + k * lo + o1), w[k].v);
     }
   }
 }
@@ -165,7 +175,11 @@ cudaError_t rope_t(RopeArgs a, int tail, cudaStream_t st) {
   a.m_tok = ((1ull << 36) + items - 1) / items;
   const int toks = a.lanes * kTok;
   const dim3 grid((a.N + toks - 1) / toks, a.B < 65535 ? a.B : 65535, (a.B + 65534) / 65535);
-  k_rope<T, W><<<grid, kRopeThreads, (size_t)toks * a.R * sizeof(float2), st>>>(a);
+  // moved bytes beyond twice L2 (126 MB): 1.41 -> 1.34 ms at 512K tokens of 32
+  // heads of 128; below that what was rotated may still be read from L2
+  const bool stream = 2.0 * a.B * a.N * a.rows * a.D * sizeof(T) > 2.5e8;
+  auto kern = stream ? k_rope<T, W, true> : k_rope<T, W, false>;
+  kern<<<grid, kRopeThreads, (size_t)toks * a.R * sizeof(float2), st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
