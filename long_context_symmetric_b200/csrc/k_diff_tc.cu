@@ -113,7 +113,7 @@ struct FwdLayout {
 
 struct FwdBars {
   uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], drain;
   uint32_t tmem_base;
   Abort abort;
 };
@@ -135,7 +135,7 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + Lay::HEAD + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(sm);
   // long tiles of all heads first
-  const int rank = (int)blockIdx.x / g.H, h = (int)blockIdx.x % g.H, hk = h / g.G;
+  const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
   if (rank >= tiles[g.ntile].x) return;                          // whole CTA, before any set-up
   const DiffTile t = tiles[rank];
   const int nkv = t.w + 1;
@@ -155,6 +155,7 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_half[s], 4);
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_done[s], 1);
     }
@@ -217,14 +218,16 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         umma_commit(&bars->s_full[m]);
       }
     };
-    auto issue_pv = [&](int m, int j) {      // O_m += P_m V
+    auto issue_pv = [&](int m, int j, int half) {      // O_m += P_m V, 64 keys of the tile
       const uint64_t b0 = dV + (uint64_t)((j % NST) * OPB16);
       const uint32_t tS = tbase + 256 * m, tO = tS + 128;
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kk = 4 * half + k4;
           umma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1), b0 + kk * 128, IDO, (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&bars->o_done[m]);
+        }
+        if (half) umma_commit(&bars->o_done[m]);
       }
     };
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -240,17 +243,23 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     for (int j = 0; ok && j < nkv; ++j) {
       const bool more = j + 1 < nkv;
       if (!wait(&bars->v_full[j % NST], (j / NST) & 1, 34)) { ok = false; break; }
+      if (!wait(&bars->p_half[0], j & 1, 35)) { ok = false; break; }
+      tc_fence_after();
+      issue_pv(0, j, 0);
       if (!wait(&bars->p_full[0], j & 1, 35)) { ok = false; break; }
       tc_fence_after();
-      issue_pv(0, j);
+      issue_pv(0, j, 1);
       if (more) {
         if (!wait(&bars->k_full[(j + 1) % NST], ((j + 1) / NST) & 1, 33)) { ok = false; break; }
         tc_fence_after();
         issue_s(0, j + 1);
       }
+      if (!wait(&bars->p_half[1], j & 1, 35)) { ok = false; break; }
+      tc_fence_after();
+      issue_pv(1, j, 0);
       if (!wait(&bars->p_full[1], j & 1, 35)) { ok = false; break; }
       tc_fence_after();
-      issue_pv(1, j);
+      issue_pv(1, j, 1);
       if (leader) umma_commit(&bars->v_empty[j % NST]);
       if (more) {
         issue_s(1, j + 1);
@@ -290,16 +299,17 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         for (int c = 0; c < 128; ++c)
           if (c > r) s[c] = __float_as_uint(-INFINITY);
       }
-      float mq[4];
+      // eight strands, so that the chain of dependent maxima is short
+      float mq[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mq[q] = __uint_as_float(s[32 * q]);
+      for (int q = 0; q < 8; ++q) {
+        mq[q] = __uint_as_float(s[16 * q]);
 #pragma unroll
-        for (int c = 1; c < 31; c += 2)
-          mq[q] = fmax3(mq[q], __uint_as_float(s[32 * q + c]), __uint_as_float(s[32 * q + c + 1]));
-        mq[q] = fmaxf(mq[q], __uint_as_float(s[32 * q + 31]));
+        for (int c = 1; c < 15; c += 2)
+          mq[q] = fmax3(mq[q], __uint_as_float(s[16 * q + c]), __uint_as_float(s[16 * q + c + 1]));
+        mq[q] = fmaxf(mq[q], __uint_as_float(s[16 * q + 15]));
       }
-      const float mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * c2;
+      const float mx = fmaxf(fmax3(fmax3(mq[0], mq[1], mq[2]), mq[3], mq[4]), fmax3(mq[5], mq[6], mq[7])) * c2;
       float m_new = m_run, alpha = 1.f;
       if (j == 0) {
         m_new = mx;
@@ -334,6 +344,11 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
           pk[e] = *reinterpret_cast<const uint32_t*>(&p2);
         }
         tmem_st16(cS + 32 * c, pk);
+        if (c == 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive_warp(&bars->p_half[m]);
+        }
       }
       const float2 a01 = __fadd2_rn(acc[0], acc[1]);
       l_run = l_run * alpha + (a01.x + a01.y);

@@ -42,24 +42,31 @@ constexpr int kComputeWarps = 8;
 constexpr uint32_t kX = 0, kY = 128, kAcc0 = 256, kAcc1 = 384;   // dkdv: X, Y, dV, dK
 constexpr uint32_t kQX2 = 128, kQY = 256, kQAcc = 384;           // dq: X_1 at 0, X_2, Y, dQ
 
-template <int D>
+// NA: stages of A_t (scores and last product). Two serve the dk, dv kernel (its
+// scores of tile t + 1 come in the middle of tile t), which needs the room for
+// the statistics; the dq kernel, whose scores come first, has three.
+constexpr int kVecStages = 3, kVecFloats = 4 * 128 + 4;
+template <int D, int NA>
 struct BwdLayout {
   static constexpr int SUB = D / 64;
   static constexpr int OPB = SUB * kDSub;
-  static constexpr int NSTA = 3, NSTB = 2;          // stages of A_t (scores and last product), B_t
+  static constexpr int NSTA = NA, NSTB = 2;         // stages of A_t, B_t
   static constexpr int FIX0 = 0, FIX1 = OPB, RA = 2 * OPB, RB = RA + NSTA * OPB;
   static constexpr int TILES = RB + NSTB * OPB;
-  // barriers, the queries' statistics (dkdv, 2 KB), up to the next 1,024-byte
-  // boundary: with the tiles of D = 128 that is all of a CTA's shared memory, so
-  // there is no slack to align the base in (base_ok checks it)
-  static constexpr int HEAD = 3072;
+  // barriers, the queries' statistics (NA = 2), up to the next 1,024-byte
+  // boundary. With three stages of D = 128 that is all of a CTA's shared memory,
+  // so there is no slack to align the base in (base_ok checks it).
+  static constexpr int VEC = 256;
+  static constexpr int HEAD = NA == 2 ? 7168 : 1024;
   static constexpr int BYTES = HEAD + TILES;
+  static_assert(NA != 2 || VEC + kVecStages * kVecFloats * 4 <= HEAD, "statistics");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 struct BwdBars {
   uint64_t fix_full, ring_full[kStages][2], ring_empty[kStages][2];
   uint64_t x_full[2], x_free[2], y_full, ds1_ready, dk1_done, p_ready, ds_ready, done, drain;
+  uint64_t vec_full[kVecStages], vec_empty[kVecStages];
   uint32_t tmem_base;
   Abort abort;
 };
@@ -107,6 +114,10 @@ __device__ __forceinline__ void bwd_setup(BwdBars* bars, int warp) {
       mbar_init(&bars->x_full[s], 1);
       mbar_init(&bars->x_free[s], kComputeWarps);
     }
+    for (int s = 0; s < kVecStages; ++s) {
+      mbar_init(&bars->vec_full[s], 1);
+      mbar_init(&bars->vec_empty[s], kComputeWarps);
+    }
     mbar_init(&bars->y_full, 1);
     mbar_init(&bars->ds1_ready, kComputeWarps);
     mbar_init(&bars->dk1_done, 1);
@@ -139,11 +150,10 @@ __device__ __forceinline__ void bwd_teardown(uint32_t tbase, int warp) {
 
 // The two fixed tiles (rows frow .. of head fh), then n streamed tiles: step t
 // reads rows row0 + (t % per) * 128 of head h0 + t / per.
-template <int D>
+template <typename Lay>
 __device__ void bwd_produce(uint8_t* sm, BwdBars* bars, const CUtensorMap* f0, const CUtensorMap* f1, int frow, int fh,
                             const CUtensorMap* ma, const CUtensorMap* mb, int row0, int per, int h0, int n,
                             volatile Abort* ab, int* err) {
-  using Lay = BwdLayout<D>;
   constexpr int SUB = Lay::SUB, NSTA = Lay::NSTA, NSTB = Lay::NSTB;
   mbar_expect_tx(&bars->fix_full, 2 * Lay::OPB);
   for (int c = 0; c < SUB; ++c) {
@@ -184,9 +194,8 @@ __device__ void bwd_produce(uint8_t* sm, BwdBars* bars, const CUtensorMap* f0, c
 }
 
 // Descriptors and waits of the issuing warp (all lanes wait, one issues).
-template <int D>
+template <int D, typename Lay>
 struct Issuer {
-  using Lay = BwdLayout<D>;
   static constexpr uint32_t IDX = idesc_f16(128, 128, false);
   static constexpr uint32_t IDV = idesc_f16(128, D, true), IDM = idesc_f16(128, D / 2, true);
   static constexpr uint32_t OPB16 = Lay::OPB >> 4;
@@ -306,11 +315,11 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
                const uint32_t* __restrict__ amax, const uint32_t* __restrict__ amax_do, const float* __restrict__ lse,
                const float* __restrict__ delta, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, float c2,
                float scale, int* err) {
-  using Lay = BwdLayout<D>;
+  using Lay = BwdLayout<D, 2>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
-  const int rank = (int)blockIdx.x / g.Hk, hk = (int)blockIdx.x % g.Hk;
+  const int rank = (int)blockIdx.x % g.ntile, hk = (int)blockIdx.x / g.ntile;
   if (rank >= tiles[g.ntile].x) return;
   if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
   const DiffTile tl = tiles[rank];
@@ -324,9 +333,9 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0)
-      bwd_produce<D>(sm, bars, &tk, &tv, tl.z + j * 128, hk, &tq, &tdo, tl.z + j * 128, per, hk * g.G, n, ab, err);
+      bwd_produce<Lay>(sm, bars, &tk, &tv, tl.z + j * 128, hk, &tq, &tdo, tl.z + j * 128, per, hk * g.G, n, ab, err);
   } else if (warp == 1) {
-    Issuer<D> is(sm, bars, ab, err);
+    Issuer<D, Lay> is(sm, bars, ab, err);
     const uint32_t tX = tbase + kX, tY = tbase + kY;
     auto ds_at = [&](int kk) -> uint32_t { return tY + 32 * (kk >> 1) + 8 * (kk & 1); };
     bool ok = is.wait(&bars->fix_full, 0, 42) && is.ring(0, 0);
@@ -357,10 +366,10 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       if (!ok) break;
       tc_fence_after();
       if (is.leader) {
-        const uint64_t b0 = is.dBm + (uint64_t)((t % Lay::NSTB) * Issuer<D>::OPB16);
+        const uint64_t b0 = is.dBm + (uint64_t)((t % Lay::NSTB) * Issuer<D, Lay>::OPB16);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts(tbase + kAcc0, ds_at(kk) + 16, b0 + kk * 128, Issuer<D>::IDV, (t > 0 || kk > 0) ? 1u : 0u);
+          umma_f16_ts(tbase + kAcc0, ds_at(kk) + 16, b0 + kk * 128, Issuer<D, Lay>::IDV, (t > 0 || kk > 0) ? 1u : 0u);
       }
       is.commit(&bars->ring_empty[t % Lay::NSTB][1]);
       ok = is.wait(&bars->ds_ready, t & 1, 47);
@@ -375,6 +384,41 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       }
     }
     is.finish(ok);
+  } else if (warp == 2) {
+    // the queries' statistics, a few tiles ahead of the compute warps: [0] -lse 1,
+    // [1] -lse 2 + log2 |lam| (both + sp), [2] -d1, [3] -d2 in dS units and signed
+    // like the map in A1 - lam A2; then that sign. Rows past the end: zeros, so
+    // that dS = 0 there.
+    const size_t rows = (size_t)g.ntile * 128;
+    const float f = pow2f(pw.sh - pw.sp), md = -pow2f(-(pw.edo + pw.ev)) * f, fsp = (float)pw.sp;
+    int i = j, h = hk * g.G;
+    for (int t = 0; t < n; ++t) {
+      const int st = t % kVecStages;
+      if (t >= kVecStages &&
+          !__all_sync(0xffffffffu, mbar_wait(&bars->vec_empty[st], ((t / kVecStages) - 1) & 1, ab, err, 52)))
+        break;
+      float* vec = reinterpret_cast<float*>(smem_raw + Lay::VEC) + st * kVecFloats;
+      const float l = __bfloat162float(lam[h]), sg = l > 0.f ? -1.f : 1.f, ll = log2f(fabsf(l));
+      const int q = i * 128 + 4 * lane;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int mp = v & 1;
+        const float4 x = *reinterpret_cast<const float4*>((v < 2 ? lse : delta) + ((size_t)h * 2 + mp) * rows + tl.z + q);
+        const float add = fsp + (mp ? ll : 0.f), mul = md * (mp ? sg : 1.f);
+        float4 y;
+        y.x = q < tl.y ? (v < 2 ? add - x.x : x.x * mul) : 0.f;
+        y.y = q + 1 < tl.y ? (v < 2 ? add - x.y : x.y * mul) : 0.f;
+        y.z = q + 2 < tl.y ? (v < 2 ? add - x.z : x.z * mul) : 0.f;
+        y.w = q + 3 < tl.y ? (v < 2 ? add - x.w : x.w * mul) : 0.f;
+        *reinterpret_cast<float4*>(vec + 128 * v + 4 * lane) = y;
+      }
+      if (lane == 0) vec[512] = sg;
+      mbar_arrive_warp(&bars->vec_full[st]);
+      if (++i == nt) {
+        i = j;
+        ++h;
+      }
+    }
   } else if (warp >= 4) {
     regs_take();
     const int quarter = warp & 3;
@@ -382,132 +426,101 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     const int m = quarter * 32 + lane;                  // key row within the tile / TMEM lane
     const uint32_t la = (uint32_t)(quarter * 32) << 16;
     const uint32_t cX = tbase + la + kX + 64 * half, cY = tbase + la + kY + 64 * half;
-    // the statistics of this half's 64 query columns: [0] -lse 1, [1] -lse 2 (+ sp),
-    // [2] -d1, [3] -d2 in dS units; thread hid fetches rows hid / 64 and 2 + hid / 64
-    float* vec = reinterpret_cast<float*>(smem_raw + 256) + 256 * half;
-    const int hid = threadIdx.x & 127, vr = hid >> 6, vc = hid & 63;
-    const size_t rows = (size_t)g.ntile * 128;
-    const float f = pow2f(pw.sh - pw.sp), md = -pow2f(-(pw.edo + pw.ev)) * f, fsp = (float)pw.sp;
+    const float f = pow2f(pw.sh - pw.sp);
     c2 *= pow2f(pw.eq + pw.ek);
-    int fi = 0, fh = hk * g.G;                          // the tile that is fetched next
-    float n0, n1;
-    auto fetch = [&]() {
-      const int q = (j + fi) * 128 + 64 * half + vc;
-      const size_t at = ((size_t)fh * 2 + vr) * rows + tl.z + q;
-      const bool in = q < tl.y;                         // rows past the end: zeros, so dS = 0 there
-      n0 = in ? fsp - lse[at] : 0.f;
-      n1 = in ? delta[at] * md : 0.f;
-      if (++fi == per) {
-        fi = 0;
-        ++fh;
-      }
-    };
-    fetch();
     bool ok = true;
-    int i = j, h = hk * g.G;
-    float nlam = -__bfloat162float(lam[h]);
-    // every compute thread runs all n steps (and their named barriers), after a
-    // wind-down too, so no warp is left waiting at a barrier
+    int i = j;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, err, site));
+    };
     for (int t = 0; t < n; ++t) {
-      named_bar_sync(1 + half, 128);                    // the half is done with the last tile's statistics
-      vec[64 * vr + vc] = n0;
-      vec[128 + 64 * vr + vc] = n1;
-      named_bar_sync(1 + half, 128);
-      if (t + 1 < n) fetch();
       const bool diag = i == j;
       const bool zero = diag && i == 0 && half == 0;    // column 0 is the sequence's first query: dS = 0
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_full[0], t & 1, ab, err, 48));
-      if (ok) {
-        tc_fence_after();
-        uint32_t p0[32], p1[32], d0[32], d1[32], pk[16];
-        tmem_ld32(cX, p0);
-        tmem_ld32(cX + 32, p1);
-        tmem_wait_ld_regs(p0);
-        reg_fence32(p1);
-        tc_fence_before();
-        mbar_arrive_warp(&bars->x_free[0]);
-        if (diag) {
-          map_cols<true>(p0, vec, c2, 64 * half, m);
-          map_cols<true>(p1, vec + 32, c2, 64 * half + 32, m);
-        } else {
-          map_cols<false>(p0, vec, c2, 0, 0);
-          map_cols<false>(p1, vec + 32, c2, 0, 0);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->y_full, t & 1, ab, err, 49));
-        if (ok) {
-          tc_fence_after();
-          tmem_ld32(cY, d0);
-          tmem_ld32(cY + 32, d1);
-          tmem_wait_ld_regs(d0);
-          reg_fence32(d1);
-          ds_cols(p0, d0, vec + 128, f, pk);
-          if (zero) pk[0] &= 0xFFFF0000u;
-          tmem_st16(cY, pk);
-          ds_cols(p1, d1, vec + 160, f, pk);
-          tmem_st16(cY + 32, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive_warp(&bars->ds1_ready);
-          // A1 waits as fp16 pairs in the columns of A1 - lam A2 (fp32 would take 64
-          // more registers; its rounding, 2^-12 of A1, is half of the sum's own)
-          uint32_t a0[16], a1[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            a0[e] = pack_f16(__uint_as_float(p0[2 * e]), __uint_as_float(p0[2 * e + 1]));
-            a1[e] = pack_f16(__uint_as_float(p1[2 * e]), __uint_as_float(p1[2 * e + 1]));
-          }
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->x_full[1], t & 1, ab, err, 48));
-          if (ok) {
-            tc_fence_after();
-            tmem_ld32(cX, p0);
-            tmem_ld32(cX + 32, p1);
-            tmem_wait_ld_regs(p0);
-            reg_fence32(p1);
-            tc_fence_before();
-            mbar_arrive_warp(&bars->x_free[1]);
-            if (diag) {
-              map_cols<true>(p0, vec + 64, c2, 64 * half, m);
-              map_cols<true>(p1, vec + 96, c2, 64 * half + 32, m);
-            } else {
-              map_cols<false>(p0, vec + 64, c2, 0, 0);
-              map_cols<false>(p1, vec + 96, c2, 0, 0);
-            }
-            // p: -lam A2; A1 - lam A2 into its columns
-            const float2 nl2 = make_float2(nlam, nlam);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = __fmul2_rn(f2(p0[2 * e], p0[2 * e + 1]), nl2), y = __fmul2_rn(f2(p1[2 * e], p1[2 * e + 1]), nl2);
-              p0[2 * e] = __float_as_uint(x.x);
-              p0[2 * e + 1] = __float_as_uint(x.y);
-              p1[2 * e] = __float_as_uint(y.x);
-              p1[2 * e + 1] = __float_as_uint(y.y);
-              a0[e] = h2_bits(__float22half2_rn(__fadd2_rn(__half22float2(*reinterpret_cast<const __half2*>(&a0[e])), x)));
-              a1[e] = h2_bits(__float22half2_rn(__fadd2_rn(__half22float2(*reinterpret_cast<const __half2*>(&a1[e])), y)));
-            }
-            tmem_st16(cY + 16, a0);
-            tmem_st16(cY + 48, a1);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive_warp(&bars->p_ready);
-            ds_cols(p0, d0, vec + 192, f, a0);
-            if (zero) a0[0] &= 0xFFFF0000u;
-            ds_cols(p1, d1, vec + 224, f, a1);
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->dk1_done, t & 1, ab, err, 50));
-            if (ok) {
-              tc_fence_after();
-              tmem_st16(cY, a0);
-              tmem_st16(cY + 32, a1);
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive_warp(&bars->ds_ready);
-            }
-          }
-        }
+      const float* vec = reinterpret_cast<const float*>(smem_raw + Lay::VEC) + (t % kVecStages) * kVecFloats + 64 * half;
+      ok = wait(&bars->vec_full[t % kVecStages], (t / kVecStages) & 1, 53) && wait(&bars->x_full[0], t & 1, 48);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t p0[32], p1[32], d0[32], d1[32], pk[16];
+      tmem_ld32(cX, p0);
+      tmem_ld32(cX + 32, p1);
+      tmem_wait_ld_regs(p0);
+      reg_fence32(p1);
+      tc_fence_before();
+      mbar_arrive_warp(&bars->x_free[0]);
+      if (diag) {
+        map_cols<true>(p0, vec, c2, 64 * half, m);
+        map_cols<true>(p1, vec + 32, c2, 64 * half + 32, m);
+      } else {
+        map_cols<false>(p0, vec, c2, 0, 0);
+        map_cols<false>(p1, vec + 32, c2, 0, 0);
       }
-      if (++i == nt) {
-        i = j;
-        if (++h < (hk + 1) * g.G) nlam = -__bfloat162float(lam[h]);
+      ok = wait(&bars->y_full, t & 1, 49);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(cY, d0);
+      tmem_ld32(cY + 32, d1);
+      tmem_wait_ld_regs(d0);
+      reg_fence32(d1);
+      ds_cols(p0, d0, vec + 256, f, pk);
+      if (zero) pk[0] &= 0xFFFF0000u;
+      tmem_st16(cY, pk);
+      ds_cols(p1, d1, vec + 288, f, pk);
+      tmem_st16(cY + 32, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_warp(&bars->ds1_ready);
+      // A1 waits as fp16 pairs in the columns of A1 - lam A2 (fp32 would take 32
+      // more registers; its rounding, 2^-12 of A1, is half of the sum's own)
+      uint32_t a0[16], a1[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        a0[e] = pack_f16(__uint_as_float(p0[2 * e]), __uint_as_float(p0[2 * e + 1]));
+        a1[e] = pack_f16(__uint_as_float(p1[2 * e]), __uint_as_float(p1[2 * e + 1]));
       }
+      ok = wait(&bars->x_full[1], t & 1, 48);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(cX, p0);
+      tmem_ld32(cX + 32, p1);
+      tmem_wait_ld_regs(p0);
+      reg_fence32(p1);
+      tc_fence_before();
+      mbar_arrive_warp(&bars->x_free[1]);
+      if (diag) {
+        map_cols<true>(p0, vec + 128, c2, 64 * half, m);
+        map_cols<true>(p1, vec + 160, c2, 64 * half + 32, m);
+      } else {
+        map_cols<false>(p0, vec + 128, c2, 0, 0);
+        map_cols<false>(p1, vec + 160, c2, 0, 0);
+      }
+      // p: |lam| A2; A1 - lam A2 into its columns
+      const float s2 = vec[512 - 64 * half];
+      const float2 sg2 = make_float2(s2, s2);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        a0[e] = h2_bits(__float22half2_rn(
+            __ffma2_rn(f2(p0[2 * e], p0[2 * e + 1]), sg2, __half22float2(*reinterpret_cast<const __half2*>(&a0[e])))));
+        a1[e] = h2_bits(__float22half2_rn(
+            __ffma2_rn(f2(p1[2 * e], p1[2 * e + 1]), sg2, __half22float2(*reinterpret_cast<const __half2*>(&a1[e])))));
+      }
+      tmem_st16(cY + 16, a0);
+      tmem_st16(cY + 48, a1);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_warp(&bars->p_ready);
+      ds_cols(p0, d0, vec + 384, f * s2, a0);
+      if (zero) a0[0] &= 0xFFFF0000u;
+      ds_cols(p1, d1, vec + 416, f * s2, a1);
+      mbar_arrive_warp(&bars->vec_empty[t % kVecStages]);
+      ok = wait(&bars->dk1_done, t & 1, 50);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_st16(cY, a0);
+      tmem_st16(cY + 32, a1);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_warp(&bars->ds_ready);
+      if (++i == nt) i = j;
     }
     if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->done, 0, ab, err, 51))) {
       tc_fence_after();
@@ -572,11 +585,11 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
              const __nv_bfloat16* __restrict__ lam, const DiffTile* __restrict__ tiles, const int* __restrict__ seq,
              const uint32_t* __restrict__ amax, const uint32_t* __restrict__ amax_do, const float* __restrict__ lse,
              const float* __restrict__ delta, __nv_bfloat16* __restrict__ dq, float c2, float scale, int* err) {
-  using Lay = BwdLayout<D>;
+  using Lay = BwdLayout<D, 3>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
-  const int rank = (int)blockIdx.x / g.H, h = (int)blockIdx.x % g.H, hk = h / g.G;
+  const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
   if (rank >= tiles[g.ntile].x) return;
   if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
   const DiffTile tl = tiles[rank];
@@ -588,9 +601,9 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
   volatile Abort* ab = &bars->abort;
   if (warp < 4) regs_give();
   if (warp == 0) {
-    if (lane == 0) bwd_produce<D>(sm, bars, &tq, &tdo, tl.z + tl.w * 128, h, &tk, &tv, tl.z, n, hk, n, ab, err);
+    if (lane == 0) bwd_produce<Lay>(sm, bars, &tq, &tdo, tl.z + tl.w * 128, h, &tk, &tv, tl.z, n, hk, n, ab, err);
   } else if (warp == 1) {
-    Issuer<D> is(sm, bars, ab, err);
+    Issuer<D, Lay> is(sm, bars, ab, err);
     // the fixed tiles belong to head h, the streamed ones to hk; operands of
     // slice kk: dS_1 at 16 kk, dS_2 behind it at 16 kk + 8
     auto ds1_at = [&](int kk) -> uint32_t { return tbase + kQY + 16 * kk; };
@@ -839,13 +852,13 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
   if (!make_tmap_16(&tq, b.qs, D, rows, g.H, true, 128) || !make_tmap_16(&tk, b.ks, D, rows, g.Hk, true, 128) ||
       !make_tmap_16(&tv, b.vs, D, rows, g.Hk, true, 128) || !make_tmap_16(&tdo, b.dos, D, rows, g.H, true, 128))
     return cudaErrorInvalidValue;
-  const int smem = BwdLayout<D>::BYTES;
+  const int smem = BwdLayout<D, 2>::BYTES, smem_q = BwdLayout<D, 3>::BYTES;
   cudaError_t e = diff_regs_ok(k_diff_dkdv_tc<D>);
   if (e != cudaSuccess) return e;
   if ((e = diff_regs_ok(k_diff_dq_tc<D>)) != cudaSuccess) return e;
   e = cudaFuncSetAttribute(k_diff_dkdv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_diff_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(k_diff_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
   if (e != cudaSuccess) return e;
   const float scale = (float)(1.0 / sqrt((double)(D / 2)));
   const float c2 = (float)(1.4426950408889634 / sqrt((double)(D / 2)));
@@ -858,7 +871,7 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
   k_diff_dkdv_tc<D><<<g.ntile * g.Hk, kDiffThreads, smem, s>>>(tk, tv, tq, tdo, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
                                                            b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_dq_tc<D><<<g.ntile * g.H, kDiffThreads, smem, s>>>(tq, tdo, tk, tv, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
+  k_diff_dq_tc<D><<<g.ntile * g.H, kDiffThreads, smem_q, s>>>(tq, tdo, tk, tv, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
                                                         b.delta, (__nv_bfloat16*)dq, c2, scale, err);
   count_launch(4);
   return cudaGetLastError();
