@@ -18,6 +18,15 @@
 // row statistics in two kernels, one per query tile (dq) and one per key tile
 // (dk, dv; it walks the query tiles of every head that shares the key/value
 // head, so shared heads need no atomics either).
+//
+// Few tiles leave most of the GPU idle and the longest causal row of tiles sets
+// the time. Then a cluster of up to 8 blocks shares one tile (split_of): block r
+// takes every r-th tile of the walk, leaves its sums in its shared memory, and
+// each block adds up an equal share of the rows from all of them, in rank order
+// (forward pass: after scaling to the common maximum). 1,021 tokens of 4 heads of
+// 64, forward and backward: 464 us without.
+#include <cooperative_groups.h>
+
 #include "k_diff.cuh"
 
 namespace lh {
@@ -27,6 +36,38 @@ constexpr int TS = kDiffTileFP;
 constexpr int NT = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int LP = TS + 4;       // row of a 64 x 64 tile
+constexpr int kMaxSplit = 8;
+
+namespace cg = cooperative_groups;
+
+// Blocks per tile: enough for two on every SM, no more than the longest walk has
+// tiles.
+int split_of(int blocks, int T) {
+  int s = 1;
+  while (s < kMaxSplit && blocks * s < 2 * 148 && 2 * s * TS <= T + TS) s *= 2;
+  return s;
+}
+
+// The sum over the cluster's blocks of one float4 at the same place of their
+// shared memory.
+__device__ __forceinline__ float4 sum_ranks(cg::cluster_group& cl, float* p, int ranks) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r = 0; r < ranks; ++r) {
+    const float4 b = *reinterpret_cast<const float4*>(cl.map_shared_rank(p, r));
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+  }
+  return a;
+}
+template <typename T>
+__device__ __forceinline__ void put4(T* d, const float4& a) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(d) = a;
+  } else {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(d);
+    h[0] = __floats2bfloat162_rn(a.x, a.y);
+    h[1] = __floats2bfloat162_rn(a.z, a.w);
+  }
+}
 
 __device__ __forceinline__ float lam_of(const void* lam, int h, const float*) { return static_cast<const float*>(lam)[h]; }
 __device__ __forceinline__ float lam_of(const void* lam, int h, const __nv_bfloat16*) {
@@ -135,12 +176,14 @@ __device__ __forceinline__ void put(T* row, int tx, const float (&v)[W]) {
 template <typename T, int D>
 __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* __restrict__ q, const T* __restrict__ k,
                                                     const T* __restrict__ v, const void* lam, const DiffTile* tiles,
-                                                    T* __restrict__ o, float* __restrict__ om, float* __restrict__ lse) {
+                                                    T* __restrict__ o, float* __restrict__ om, float* __restrict__ lse,
+                                                    int split) {
   constexpr int LD = D + 4, W = D / 16, DM = D / 2;
   extern __shared__ __align__(16) float smf[];
   float *Q = smf, *K = Q + TS * LD, *V = K + TS * LD, *P = V + TS * LD;    // P: two maps
-  if (blockIdx.x >= tiles[g.ntile].x) return;
-  const DiffTile t = tiles[blockIdx.x];
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  if (tile >= tiles[g.ntile].x) return;           // the whole cluster
+  const DiffTile t = tiles[tile];
   const int h = blockIdx.y, hk = h / g.G;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = t.w * TS;                                // first row within the sequence
@@ -158,7 +201,7 @@ __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* _
 #pragma unroll
       for (int c = 0; c < W; ++c) acc[u][i][c] = 0.f;
     }
-  for (int n0 = 0; n0 <= r0; n0 += TS) {
+  for (int n0 = rank * TS; n0 <= r0; n0 += split * TS) {
     __syncthreads();
     stage<T, D>(K, kb, g.ldk, n0, t.y);
     stage<T, D>(V, vb, g.ldv, n0, t.y);
@@ -195,6 +238,53 @@ __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* _
     for (int u = 0; u < 2; ++u) mm_nn<W, LD>(P + u * TS * LP, V, ty, tx, acc[u]);
   }
   const float la = lam_of(lam, h, q);
+  if (split > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    float *A = smf, *M = smf + 2 * TS * LD;       // [2][64][LD] sums, then [4][64]: maxima and sums of both maps
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = ty * 4 + i;
+#pragma unroll
+        for (int c = 0; c < W; ++c) A[(u * TS + rr) * LD + ncol<W>(c, tx)] = acc[u][i][c];
+        if (tx == 0) {
+          M[u * TS + rr] = m[u][i];
+          M[(2 + u) * TS + rr] = l[u][i];
+        }
+      }
+    cl.sync();
+    const int share = TS / split;
+    for (int x = threadIdx.x; x < share * (D / 4); x += NT) {
+      const int rr = rank * share + x / (D / 4), c = (x % (D / 4)) * 4, r = r0 + rr;
+      if (r >= t.y) continue;
+      const long long row = t.x + r;
+      float4 both[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float mx = -INFINITY, sum = 0.f;
+        for (int k = 0; k < split; ++k) mx = fmaxf(mx, *cl.map_shared_rank(M + u * TS + rr, k));
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < split; ++k) {
+          // a block that had no tile has maximum -inf and sums of 0: weight 0
+          const float w = exp2f(*cl.map_shared_rank(M + u * TS + rr, k) - mx);
+          const float4 b = *reinterpret_cast<const float4*>(cl.map_shared_rank(A + (u * TS + rr) * LD + c, k));
+          sum = fmaf(w, *cl.map_shared_rank(M + (2 + u) * TS + rr, k), sum);
+          a.x = fmaf(w, b.x, a.x); a.y = fmaf(w, b.y, a.y); a.z = fmaf(w, b.z, a.z); a.w = fmaf(w, b.w, a.w);
+        }
+        const float inv = 1.f / sum;
+        // rounded products, so that o is the same whether they are stored or not
+        both[u] = make_float4(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv), __fmul_rn(a.z, inv), __fmul_rn(a.w, inv));
+        if (om) put4(om + ((row * g.H + h) * 2 + u) * D + c, both[u]);
+        if (lse && c == 0) lse[(2LL * h + u) * g.T + row] = mx + log2f(sum);
+      }
+      put4(o + row * g.ldo + (long long)h * D + c,
+           make_float4(both[0].x - la * both[1].x, both[0].y - la * both[1].y, both[0].z - la * both[1].z, both[0].w - la * both[1].w));
+    }
+    cl.sync();        // nobody leaves while its sums are still read
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + ty * 4 + i;
@@ -204,8 +294,8 @@ __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* _
     const float i0 = 1.f / l[0][i], i1 = 1.f / l[1][i];
 #pragma unroll
     for (int c = 0; c < W; ++c) {
-      a[c] = acc[0][i][c] * i0;
-      b[c] = acc[1][i][c] * i1;
+      a[c] = __fmul_rn(acc[0][i][c], i0);      // rounded: o is the same whether they are stored or not
+      b[c] = __fmul_rn(acc[1][i][c], i1);
       both[c] = a[c] - la * b[c];
     }
     put<W>(o + row * g.ldo + (long long)h * D, tx, both);
@@ -266,12 +356,13 @@ template <typename T, int D>
 __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __restrict__ dout, const T* __restrict__ q,
                                                    const T* __restrict__ k, const T* __restrict__ v, const void* lam,
                                                    const DiffTile* tiles, const float* __restrict__ lse,
-                                                   const float* __restrict__ delta, T* __restrict__ dq) {
+                                                   const float* __restrict__ delta, T* __restrict__ dq, int split) {
   constexpr int LD = D + 4, DM = D / 2, W = DM / 16;
   extern __shared__ __align__(16) float smf[];
   float *Q = smf, *O = Q + TS * LD, *K = O + TS * LD, *V = K + TS * LD, *S = V + TS * LD;
-  if (blockIdx.x >= tiles[g.ntile].x) return;
-  const DiffTile t = tiles[blockIdx.x];
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  if (tile >= tiles[g.ntile].x) return;           // the whole cluster
+  const DiffTile t = tiles[tile];
   const int h = blockIdx.y, hk = h / g.G;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = t.w * TS;
@@ -290,7 +381,7 @@ __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __
       ls[u][i] = r < t.y ? lse[at] : 0.f;
       dl[u][i] = r < t.y ? delta[at] : 0.f;
     }
-  for (int n0 = 0; n0 <= r0; n0 += TS) {
+  for (int n0 = rank * TS; n0 <= r0; n0 += split * TS) {
     __syncthreads();
     stage<T, D>(K, kb, g.ldk, n0, t.y);
     stage<T, D>(V, vb, g.ldv, n0, t.y);
@@ -316,6 +407,25 @@ __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __
 #pragma unroll
     for (int u = 0; u < 2; ++u) mm_nn<W, LD>(S + u * TS * LP, K + u * DM, ty, tx, acc[u]);
   }
+  if (split > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    float* A = smf;                                 // [64][LD]
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < W; ++c) A[(ty * 4 + i) * LD + u * DM + ncol<W>(c, tx)] = acc[u][i][c];
+    cl.sync();
+    const int share = TS / split;
+    for (int x = threadIdx.x; x < share * (D / 4); x += NT) {
+      const int rr = rank * share + x / (D / 4), c = (x % (D / 4)) * 4;
+      if (r0 + rr < t.y) put4(dq + (t.x + (long long)(r0 + rr)) * g.ldq + (long long)h * D + c, sum_ranks(cl, A + rr * LD + c, split));
+    }
+    cl.sync();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + ty * 4 + i;
@@ -331,12 +441,13 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
                                                      const T* __restrict__ q, const T* __restrict__ k,
                                                      const T* __restrict__ v, const void* lam, const DiffTile* tiles,
                                                      const float* __restrict__ lse, const float* __restrict__ delta,
-                                                     T* __restrict__ dk, T* __restrict__ dv) {
+                                                     T* __restrict__ dk, T* __restrict__ dv, int split) {
   constexpr int LD = D + 4, DM = D / 2, W = DM / 16, WV = D / 16;
   extern __shared__ __align__(16) float smf[];
   float *K = smf, *V = K + TS * LD, *Q = V + TS * LD, *O = Q + TS * LD, *S = O + TS * LD, *vec = S + TS * LP;
-  if (blockIdx.x >= tiles[g.ntile].x) return;
-  const DiffTile t = tiles[blockIdx.x];
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  if (tile >= tiles[g.ntile].x) return;
+  const DiffTile t = tiles[tile];
   const int ntl = (t.y + TS - 1) / TS, jt = ntl - 1 - t.w;      // early key tiles first: they have the most queries
   const int hk = blockIdx.y;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -345,9 +456,12 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
   stage<T, D>(K, k + (long long)t.x * g.ldk + (long long)hk * D, g.ldk, k0, t.y);
   stage<T, D>(V, v + (long long)t.x * g.ldv + (long long)hk * D, g.ldv, k0, t.y);
   float aV[4][WV] = {}, aK[2][4][W] = {};
-  for (int h = hk * g.G; h < (hk + 1) * g.G; ++h) {
-    const float la = lam_of(lam, h, q);
-    for (int i0 = k0; i0 < t.y; i0 += TS) {
+  {
+    // the query tiles from this one on, of every head that shares the key head
+    const int per = ntl - jt;
+    for (int it = rank; it < per * g.G; it += split) {
+      const int h = hk * g.G + it / per, i0 = k0 + (it % per) * TS;
+      const float la = lam_of(lam, h, q);
       __syncthreads();
       stage<T, D>(Q, q + (long long)t.x * g.ldq + (long long)h * D, g.ldq, i0, t.y);
       stage<T, D>(O, dout + (long long)t.x * g.ldo + (long long)h * D, g.ldo, i0, t.y);
@@ -388,6 +502,31 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
       mm_nn<WV, LD>(S, O, ty, tx, aV);
     }
   }
+  if (split > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    float *A = smf, *B = smf + TS * LD;             // dk, dv: [64][LD] each
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < W; ++c) A[(ty * 4 + i) * LD + u * DM + ncol<W>(c, tx)] = aK[u][i][c];
+#pragma unroll
+      for (int c = 0; c < WV; ++c) B[(ty * 4 + i) * LD + ncol<WV>(c, tx)] = aV[i][c];
+    }
+    cl.sync();
+    const int share = TS / split;
+    for (int x = threadIdx.x; x < share * (D / 4); x += NT) {
+      const int rr = rank * share + x / (D / 4), c = (x % (D / 4)) * 4;
+      if (k0 + rr >= t.y) continue;
+      const long long row = t.x + k0 + rr;
+      put4(dk + row * g.ldk + (long long)hk * D + c, sum_ranks(cl, A + rr * LD + c, split));
+      put4(dv + row * g.ldv + (long long)hk * D + c, sum_ranks(cl, B + rr * LD + c, split));
+    }
+    cl.sync();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = k0 + ty * 4 + i;
@@ -399,6 +538,24 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
   }
 }
 
+// grid (tiles * split, heads), clusters of `split` blocks along x
+template <typename K, typename... A>
+cudaError_t launch_split(K kern, int ntile, int heads, int split, int sm, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(ntile * split, heads);
+  c.blockDim = dim3(NT);
+  c.dynamicSmemBytes = sm;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&c, kern, args..., split);
+}
+
 template <typename T, int D>
 cudaError_t fwd_t(const DiffGeom& g, const void* q, const void* k, const void* v, const void* lam, const DiffTile* tiles,
                   void* o, float* om, float* lse, cudaStream_t s) {
@@ -406,9 +563,8 @@ cudaError_t fwd_t(const DiffGeom& g, const void* q, const void* k, const void* v
   auto kern = k_diff_fwd_fp<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(g.ntile, g.H), NT, sm, s>>>(g, (const T*)q, (const T*)k, (const T*)v, lam, tiles, (T*)o, om, lse);
-  count_launch();
-  return cudaGetLastError();
+  return launch_split(kern, g.ntile, g.H, split_of(g.ntile * g.H, g.T), sm, s, g, (const T*)q, (const T*)k, (const T*)v, lam,
+                      tiles, (T*)o, om, lse);
 }
 
 template <typename T, int D>
@@ -422,15 +578,11 @@ cudaError_t bwd_t(const DiffGeom& g, const void* dout, const void* q, const void
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, sm2);
   if (e != cudaSuccess) return e;
-  kk<<<dim3(g.ntile, g.Hk), NT, sm2, s>>>(g, (const T*)dout, (const T*)q, (const T*)k, (const T*)v, lam, tiles, lse,
-                                          delta, (T*)dk, (T*)dv);
-  count_launch();
-  e = cudaGetLastError();
+  e = launch_split(kk, g.ntile, g.Hk, split_of(g.ntile * g.Hk, g.T * g.G), sm2, s, g, (const T*)dout, (const T*)q,
+                   (const T*)k, (const T*)v, lam, tiles, lse, delta, (T*)dk, (T*)dv);
   if (e != cudaSuccess) return e;
-  kq<<<dim3(g.ntile, g.H), NT, sm1, s>>>(g, (const T*)dout, (const T*)q, (const T*)k, (const T*)v, lam, tiles, lse,
-                                         delta, (T*)dq);
-  count_launch();
-  return cudaGetLastError();
+  return launch_split(kq, g.ntile, g.H, split_of(g.ntile * g.H, g.T), sm1, s, g, (const T*)dout, (const T*)q, (const T*)k,
+                      (const T*)v, lam, tiles, lse, delta, (T*)dq);
 }
 
 }  // namespace

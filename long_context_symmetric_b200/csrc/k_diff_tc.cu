@@ -5,7 +5,7 @@
 //
 // Working copies (k_diff_pack). q, k, v are copied once, from the caller's
 // layout into [head][padded row][D] fp16, times a power of two per sequence and
-// key/value head that brings the largest magnitude into [4, 256) (scale_exp):
+// key/value head that brings the largest magnitude into [1/8, 256) (diff_exp):
 // bf16 values enter fp16 unchanged but for that power, and P and dS may then be
 // rounded to fp16's 11 bits instead of bf16's 8, which is what keeps the
 // difference of two maps, and its gradients, at the accuracy of the bf16 results
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_
   uint32_t* am = amax + ((size_t)which * g.B + seq[blockIdx.x]) * g.Hk + hk;
   float mul = 1.f;
   if (REDO) {
-    const int e = scale_exp(*am);
+    const int e = diff_exp(*am);
     if (e == 0) return;
     mul = pow2f(-e);
   }
@@ -142,8 +142,8 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t* am = amax + (size_t)seq[rank] * g.Hk + hk;
   const size_t plane = (size_t)g.B * g.Hk;
-  const int ev = scale_exp(am[kScaleV * plane]);
-  c2 *= pow2f(scale_exp(am[kScaleQ * plane]) + scale_exp(am[kScaleK * plane]));
+  const int ev = diff_exp(am[kScaleV * plane]);
+  c2 *= pow2f(diff_exp(am[kScaleQ * plane]) + diff_exp(am[kScaleK * plane]));
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);

@@ -24,6 +24,16 @@ struct DiffTC {
   float* part;                // [H][ntile] sums of delta 2
 };
 
+// The power of two of a working copy: x 2^-e, e = 0 while the head's largest
+// magnitude is in [1/8, 256), else what brings it into [4, 8). Wider downwards
+// than scale_exp's window, so that values of ordinary size need one pass: with a
+// largest value of 1/8, bf16 values down to 2^-14 of it still enter unchanged and
+// smaller ones are off by at most 2^-22 of it.
+__host__ __device__ __forceinline__ int diff_exp(uint32_t amax_bits) {
+  const int ex = (int)((amax_bits >> 23) & 0xFFu) - 127;
+  return ex >= -3 && ex < 2 ? 0 : scale_exp(amax_bits);
+}
+
 // Registers. A CTA of three warpgroups (384 threads) is launched with 168
 // registers a thread, all that a one-CTA SM has (launch bounds 384, 1). The
 // warpgroup of the producer and the issuer gives up 96 of them, each of the two

@@ -81,10 +81,10 @@ __device__ __forceinline__ Powers powers(const DiffGeom& g, const uint32_t* amax
   const size_t plane = (size_t)g.B * g.Hk, at = (size_t)b * g.Hk + hk;
   const uint32_t av = amax[kScaleV * plane + at], ad = amax_do[at];
   Powers p;
-  p.eq = scale_exp(amax[kScaleQ * plane + at]);
-  p.ek = scale_exp(amax[kScaleK * plane + at]);
-  p.ev = scale_exp(av);
-  p.edo = scale_exp(ad);
+  p.eq = diff_exp(amax[kScaleQ * plane + at]);
+  p.ek = diff_exp(amax[kScaleK * plane + at]);
+  p.ev = diff_exp(av);
+  p.edo = diff_exp(ad);
   float lm = 0.f;
   for (int h = hk * g.G; h < (hk + 1) * g.G; ++h) lm = fmaxf(lm, fabsf(__bfloat162float(lam[h])));
   p.sp = max(-100, 13 - ilogbf(1.f + fminf(lm, 1e30f)));
@@ -770,13 +770,13 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
   const size_t sh = (size_t)seq[blockIdx.x] * g.Hk + hk;
   float mul = 1.f;
   if (REDO) {
-    const int e = scale_exp(amax_do[sh]);
+    const int e = diff_exp(amax_do[sh]);
     if (e == 0) return;
     mul = pow2f(-e);
   }
   const int r0 = t.w * 128, c = (threadIdx.x % L) * 8;
   const size_t rows = (size_t)g.ntile * 128;
-  const float pv = REDO ? 1.f : pow2f(scale_exp(amax[(size_t)kScaleV * g.B * g.Hk + sh]));
+  const float pv = REDO ? 1.f : pow2f(diff_exp(amax[(size_t)kScaleV * g.B * g.Hk + sh]));
   uint32_t mx = 0;
   float tot = 0.f;
 #pragma unroll 2

@@ -19,7 +19,6 @@
 namespace lh {
 namespace {
 
-constexpr int kRopeThreads = 64;
 constexpr int kTok = 4;               // tokens per thread, all in flight at once
 constexpr int kRopeSmem = 16384;      // cosines and sines of a block's tokens, at most (or of kTok tokens)
 
@@ -74,8 +73,8 @@ union Chunk {
 // neighbouring vectors), or two vectors of the tail. A thread takes one item of
 // kTok neighbouring tokens: the addresses are formed once for all of them.
 // STREAM: data beyond what L2 holds is marked to leave it first.
-template <typename T, int W, bool STREAM>
-__global__ void __launch_bounds__(kRopeThreads, 12) k_rope(const RopeArgs a) {
+template <typename T, int W, int TH, bool STREAM>
+__global__ void __launch_bounds__(TH, 768 / TH) k_rope(const RopeArgs a) {
   extern __shared__ float2 cs[];                       // [tokens][R]: cosine, sine
   using V = typename Pack<T, W>::V;
   const int b = blockIdx.y + blockIdx.z * 65535;
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads, 12) k_rope(const RopeArgs a) {
   const int t0 = blockIdx.x * a.lanes * kTok, items = a.rows * a.per_row;
   const int nt = min(a.lanes * kTok, a.N - t0);
   bool ready = false;
-  for (int x = threadIdx.x; x < items * a.lanes || !ready; x += kRopeThreads) {
+  for (int x = threadIdx.x; x < items * a.lanes || !ready; x += TH) {
     const int grp = a.lanes > 1 ? div36(x, a.m_tok) : 0,      // more than one only below 256 items
                y = x - grp * items, row = div36(y, a.m_row), c = y - row * a.per_row;
     const int tk = grp * kTok, live = x < items * a.lanes ? min(kTok, nt - tk) : 0;
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kRopeThreads, 12) k_rope(const RopeArgs a) {
       }
     }
     if (!ready) {
-      for (int z = threadIdx.x; z < nt * a.R; z += kRopeThreads) {
+      for (int z = threadIdx.x; z < nt * a.R; z += TH) {
         const int tok = z / a.R, i = z - tok * a.R;
         int ax = __ldg(a.axis + i);
         if (ax < 0 || ax >= a.axes) {
@@ -166,11 +165,26 @@ cudaError_t rope_t(RopeArgs a, int tail, cudaStream_t st) {
   a.per_row = a.rot_items + (tail + 2 * W - 1) / (2 * W);
   a.rows = a.H + a.Hk;
   const int items = a.rows * a.per_row;
-  a.lanes = kRopeThreads / items;
-  const int fit = kRopeSmem / (kTok * a.R * (int)sizeof(float2));
-  if (a.lanes > fit) a.lanes = fit;
-  if (a.lanes > (a.N + kTok - 1) / kTok) a.lanes = (a.N + kTok - 1) / kTok;
-  if (a.lanes < 1) a.lanes = 1;
+  // groups of tokens that a block of th threads takes
+  auto lanes_of = [&](int th) {
+    const int fit = kRopeSmem / (kTok * a.R * (int)sizeof(float2)), groups = (a.N + kTok - 1) / kTok;
+    int l = th / items;
+    l = l < fit ? l : fit;
+    l = l < groups ? l : groups;
+    return l < 1 ? 1 : l;
+  };
+  // Small blocks overlap each other's phases best: 512K tokens of 256 items, 64
+  // threads 1.34 ms, 256 threads 1.64. The larger ones where 64 threads would have
+  // too little to do in their last round (16K tokens of 80 items: 62 % of the lanes
+  // busy against 94 %), or where there are too few blocks to fill the GPU (256
+  // tokens of 256 items: 8.0 us with 64 threads, 4.2 with 256).
+  auto busy = [&](int th) {
+    const int n = items * lanes_of(th);
+    return (double)n / ((double)((n + th - 1) / th) * th);
+  };
+  const bool few = (long long)a.B * ((a.N + kTok - 1) / kTok) < 148 * 4;
+  const int th = few || busy(256) > 1.1 * busy(64) ? 256 : 64;
+  a.lanes = lanes_of(th);
   a.m_row = ((1ull << 36) + a.per_row - 1) / a.per_row;
   a.m_tok = ((1ull << 36) + items - 1) / items;
   const int toks = a.lanes * kTok;
@@ -178,8 +192,9 @@ cudaError_t rope_t(RopeArgs a, int tail, cudaStream_t st) {
   // moved bytes beyond twice L2 (126 MB): 1.41 -> 1.34 ms at 512K tokens of 32
   // heads of 128; below that what was rotated may still be read from L2
   const bool stream = 2.0 * a.B * a.N * a.rows * a.D * sizeof(T) > 2.5e8;
-  auto kern = stream ? k_rope<T, W, true> : k_rope<T, W, false>;
-  kern<<<grid, kRopeThreads, (size_t)toks * a.R * sizeof(float2), st>>>(a);
+  auto kern = th == 64 ? (stream ? k_rope<T, W, 64, true> : k_rope<T, W, 64, false>)
+                       : (stream ? k_rope<T, W, 256, true> : k_rope<T, W, 256, false>);
+  kern<<<grid, th, (size_t)toks * a.R * sizeof(float2), st>>>(a);
   count_launch();
   return cudaGetLastError();
 }

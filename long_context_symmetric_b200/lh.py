@@ -425,44 +425,54 @@ _TORCH = {LH_BF16: torch.bfloat16, LH_FP32: torch.float32}
 _NAMES = {torch.bfloat16: "bf16", torch.float32: "fp32"}
 
 
+# The current stream's handle and the current device without the objects that
+# torch.cuda.current_stream() builds around them (4 of the 12 us that a small
+# call took on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(name, dev, stream, *args):
     """One entry point, on the device that the tensors live on."""
-    f = getattr(lib(), name)
-    if dev.index is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
+    f = getattr(_lib or lib(), name)
+    if dev.type != "cuda":
+        st = f(*args, _stream(stream))
+    elif dev.index == _raw_device():
+        st = f(*args, _raw_stream(dev.index) if stream is None else _stream(stream))
+    else:
         with torch.cuda.device(dev):
             st = f(*args, _stream(stream))
-    else:
-        st = f(*args, _stream(stream))
     if st != 0:
         raise LHError(st, name)
 
 
-def _need(name, dev, *tensors):
-    """Each (label, tensor or None, dtype, elements): contiguous, of that type and at least that size."""
-    for label, t, dt, n in tensors:
-        if t is None:
-            continue
-        if t.dtype != dt:
-            raise ValueError(f"{name}: {label} has type {t.dtype}, {dt} is wanted")
-        if t.device != dev:
-            raise ValueError(f"{name}: {label} is on {t.device}, the call is on {dev}")
-        if t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"{name}: {label} of shape {tuple(t.shape)}: {n} contiguous elements are wanted")
+def _need(name, dev, label, t, dt, n):
+    """t is None, or contiguous, of type dt, on dev and at least n elements long."""
+    if t is None or (t.dtype is dt and t.device == dev and t.numel() >= n and t.is_contiguous()):
+        return
+    _refuse(name, dev, label, t, dt)
+    raise ValueError(f"{name}: {label} of shape {tuple(t.shape)}: {n} contiguous elements are wanted")
 
 
-def _span(t):
-    """Elements from a tensor's first one to the end of its storage."""
-    return t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-
-
-def _rows_fit(name, label, t, dt, dev, rows, ld, width):
+def _rows_fit(name, dev, label, t, dt, rows, ld, width):
     """rows x width elements, ld apart, lie in the tensor's storage."""
+    n = (rows - 1) * ld + width if rows else 0
+    if t.dtype is dt and t.device == dev:
+        # a contiguous tensor of that size, or room enough behind a view's first element
+        if t.numel() >= n and t.is_contiguous():
+            return
+        if n <= t.untyped_storage().nbytes() // t.element_size() - t.storage_offset():
+            return
+    _refuse(name, dev, label, t, dt)
+    raise ValueError(f"{name}: {label} ends before row {rows - 1} of {width} elements, {ld} apart")
+
+
+def _refuse(name, dev, label, t, dt):
     if t.dtype != dt:
         raise ValueError(f"{name}: {label} has type {t.dtype}, {dt} is wanted")
     if t.device != dev:
         raise ValueError(f"{name}: {label} is on {t.device}, the call is on {dev}")
-    if rows and (rows - 1) * ld + width > _span(t):
-        raise ValueError(f"{name}: {label} ends before row {rows - 1} of {width} elements, {ld} apart")
 
 
 def make_norm_config(M, d, dtype="bf16", wdtype=None, eps=1e-5, ldx=0, ldy=0) -> NormConfig:
@@ -482,23 +492,29 @@ def norm_workspace(cfg: NormConfig, device):
 
 
 def norm_fwd(cfg, x, w, b, y, mean=None, rstd=None, stream=None):
-    dev, dt, wt, M, d = x.device, _TORCH[cfg.dtype], _TORCH[cfg.wdtype], cfg.M, cfg.d
-    _rows_fit("lh_norm_fwd", "x", x, dt, dev, M, cfg.ldx or d, d)
-    _rows_fit("lh_norm_fwd", "y", y, dt, dev, M, cfg.ldy or d, d)
-    _need("lh_norm_fwd", dev, ("w", w, wt, d), ("b", b, wt, d), ("mean", mean, torch.float32, M),
-          ("rstd", rstd, torch.float32, M))
-    _call("lh_norm_fwd", dev, stream, ctypes.byref(cfg), _p(x), _p(w), _p(b), _p(y), _p(mean), _p(rstd))
+    dev, dt, wt, M, d, f = x.device, _TORCH[cfg.dtype], _TORCH[cfg.wdtype], cfg.M, cfg.d, "lh_norm_fwd"
+    _rows_fit(f, dev, "x", x, dt, M, cfg.ldx or d, d)
+    _rows_fit(f, dev, "y", y, dt, M, cfg.ldy or d, d)
+    _need(f, dev, "w", w, wt, d)
+    _need(f, dev, "b", b, wt, d)
+    _need(f, dev, "mean", mean, torch.float32, M)
+    _need(f, dev, "rstd", rstd, torch.float32, M)
+    _call(f, dev, stream, ctypes.byref(cfg), _p(x), _p(w), _p(b), _p(y), _p(mean), _p(rstd))
 
 
 def norm_bwd(cfg, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
-    dev, dt, wt, M, d = x.device, _TORCH[cfg.dtype], _TORCH[cfg.wdtype], cfg.M, cfg.d
-    _rows_fit("lh_norm_bwd", "x", x, dt, dev, M, cfg.ldx or d, d)
-    _rows_fit("lh_norm_bwd", "dx", dx, dt, dev, M, cfg.ldx or d, d)
-    _rows_fit("lh_norm_bwd", "dy", dy, dt, dev, M, cfg.ldy or d, d)
-    _need("lh_norm_bwd", dev, ("w", w, wt, d), ("mean", mean, torch.float32, M), ("rstd", rstd, torch.float32, M),
-          ("dw", dw, wt, d), ("db", db, wt, d))
-    _call("lh_norm_bwd", dev, stream, ctypes.byref(cfg), _p(dy), _p(x), _p(w), _p(mean), _p(rstd), _p(dx), _p(dw),
-          _p(db), _p(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+    dev, dt, wt, M, d, f = x.device, _TORCH[cfg.dtype], _TORCH[cfg.wdtype], cfg.M, cfg.d, "lh_norm_bwd"
+    _rows_fit(f, dev, "x", x, dt, M, cfg.ldx or d, d)
+    _rows_fit(f, dev, "dx", dx, dt, M, cfg.ldx or d, d)
+    _rows_fit(f, dev, "dy", dy, dt, M, cfg.ldy or d, d)
+    _need(f, dev, "w", w, wt, d)
+    _need(f, dev, "mean", mean, torch.float32, M)
+    _need(f, dev, "rstd", rstd, torch.float32, M)
+    _need(f, dev, "dw", dw, wt, d)
+    _need(f, dev, "db", db, wt, d)
+    _need(f, dev, "ws", ws, torch.uint8, 0)
+    _call(f, dev, stream, ctypes.byref(cfg), _p(dy), _p(x), _p(w), _p(mean), _p(rstd), _p(dx), _p(dw), _p(db), _p(ws),
+          ws.numel() if ws is not None else 0)
 
 
 ROPE_PAIRS = {"half": 0, "next": 1}
@@ -517,17 +533,18 @@ def make_rope_config(B, N, H, Hk, D, rot=None, axes=1, dtype="bf16", pairs="half
 
 def rope(cfg, q, k, pos, freq, axis, qo, ko, inverse=False, stream=None):
     """qo, ko: q and k rotated (q and k themselves: in place). inverse: the backward pass, dq and dk for q and k."""
-    dev, dt, B, N, D = q.device, _TORCH[cfg.dtype], cfg.B, cfg.N, cfg.D
+    dev, dt, B, N, D, R, f = q.device, _TORCH[cfg.dtype], cfg.B, cfg.N, cfg.D, cfg.rot // 2, "lh_rope"
     if B and N:
         for label, t, heads, ld, bs in (("q", q, cfg.H, cfg.q_ld, cfg.q_bs), ("qo", qo, cfg.H, cfg.qo_ld, cfg.qo_bs),
                                         ("k", k, cfg.Hk, cfg.k_ld, cfg.k_bs), ("ko", ko, cfg.Hk, cfg.ko_ld, cfg.ko_bs)):
             if heads:
                 ld = ld or heads * D
-                _rows_fit("lh_rope", label, t, dt, dev, 1, 0, (B - 1) * (bs or N * ld) + (N - 1) * ld + heads * D)
-        _rows_fit("lh_rope", "pos", pos, torch.int64 if cfg.pos64 else torch.int32, dev, 1, 0,
+                _rows_fit(f, dev, label, t, dt, 1, 0, (B - 1) * (bs or N * ld) + (N - 1) * ld + heads * D)
+        _rows_fit(f, dev, "pos", pos, torch.int64 if cfg.pos64 else torch.int32, 1, 0,
                   (cfg.axes - 1) * cfg.pos_as + (B - 1) * cfg.pos_bs + N)
-    _need("lh_rope", dev, ("freq", freq, torch.float64, cfg.rot // 2), ("axis", axis, torch.int32, cfg.rot // 2))
-    _call("lh_rope", dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(pos), _p(freq), _p(axis), int(inverse), _p(qo), _p(ko))
+    _need(f, dev, "freq", freq, torch.float64, R)
+    _need(f, dev, "axis", axis, torch.int32, R)
+    _call(f, dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(pos), _p(freq), _p(axis), int(inverse), _p(qo), _p(ko))
 
 
 def make_diff_config(B, N, H, D, dtype="bf16", Hk=None, rows=None, train=True, ldq=0, ldk=0, ldv=0, ldo=0) -> DiffConfig:
@@ -553,37 +570,34 @@ class DiffWorkspace:
         self.ws = torch.empty(max(pl.ws_bytes, 16), dtype=torch.uint8, device=device) if cfg.train else None
 
 
-def _diff_check(name, cfg, cu, dev, qs, ks):
-    dt, D = _TORCH[cfg.dtype], cfg.D
-    for label, t, ld, heads in qs + ks:
-        _rows_fit(name, label, t, dt, dev, cfg.T, ld or heads * D, heads * D)
+def _diff_check(f, dev, cfg, cu, lam, ws, rows):
+    dt, T, D = _TORCH[cfg.dtype], cfg.T, cfg.D
+    for label, t, ld, heads in rows:
+        _rows_fit(f, dev, label, t, dt, T, ld or heads * D, heads * D)
+    _need(f, dev, "lam", lam, dt, cfg.H)
+    _need(f, dev, "saved", ws.saved, torch.uint8, 0)
     if cfg.packed:
         if cu is None:
-            raise ValueError(f"{name}: packed sequences need cu")
-        _need(name, dev, ("cu", cu, torch.int32, cfg.B + 1))
+            raise ValueError(f"{f}: packed sequences need cu")
+        _need(f, dev, "cu", cu, torch.int32, cfg.B + 1)
 
 
 def diff_attn_fwd(cfg, q, k, v, lam, o, ws: DiffWorkspace, cu=None, stream=None):
-    dev = q.device
-    _diff_check("lh_diff_attn_fwd", cfg, cu, dev, [("q", q, cfg.ldq, cfg.H), ("o", o, cfg.ldo, cfg.H)],
-                [("k", k, cfg.ldk, cfg.Hk), ("v", v, cfg.ldv, cfg.Hk)])
-    _need("lh_diff_attn_fwd", dev, ("lam", lam, _TORCH[cfg.dtype], cfg.H), ("saved", ws.saved, torch.uint8, 0))
-    _call("lh_diff_attn_fwd", dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(v), _p(lam), _p(cu), _p(o),
-          _p(ws.saved), ws.saved.numel())
+    f, dev = "lh_diff_attn_fwd", q.device
+    _diff_check(f, dev, cfg, cu, lam, ws, (("q", q, cfg.ldq, cfg.H), ("k", k, cfg.ldk, cfg.Hk),
+                                           ("v", v, cfg.ldv, cfg.Hk), ("o", o, cfg.ldo, cfg.H)))
+    _call(f, dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(v), _p(lam), _p(cu), _p(o), _p(ws.saved), ws.saved.numel())
 
 
 def diff_attn_bwd(cfg, dout, q, k, v, lam, ws: DiffWorkspace, dq, dk, dv, dlam, cu=None, stream=None):
-    dev = q.device
-    _diff_check("lh_diff_attn_bwd", cfg, cu, dev,
-                [("q", q, cfg.ldq, cfg.H), ("dq", dq, cfg.ldq, cfg.H), ("dout", dout, cfg.ldo, cfg.H)],
-                [("k", k, cfg.ldk, cfg.Hk), ("dk", dk, cfg.ldk, cfg.Hk), ("v", v, cfg.ldv, cfg.Hk),
-                 ("dv", dv, cfg.ldv, cfg.Hk)])
-    dt = _TORCH[cfg.dtype]
-    _need("lh_diff_attn_bwd", dev, ("lam", lam, dt, cfg.H), ("dlam", dlam, dt, cfg.H),
-          ("saved", ws.saved, torch.uint8, 0), ("ws", ws.ws, torch.uint8, 0))
-    _call("lh_diff_attn_bwd", dev, stream, ctypes.byref(cfg), _p(dout), _p(q), _p(k), _p(v), _p(lam), _p(cu),
-          _p(ws.saved), ws.saved.numel(), _p(ws.ws), ws.ws.numel() if ws.ws is not None else 0, _p(dq), _p(dk),
-          _p(dv), _p(dlam))
+    f, dev = "lh_diff_attn_bwd", q.device
+    _diff_check(f, dev, cfg, cu, lam, ws,
+                (("dout", dout, cfg.ldo, cfg.H), ("q", q, cfg.ldq, cfg.H), ("dq", dq, cfg.ldq, cfg.H),
+                 ("k", k, cfg.ldk, cfg.Hk), ("dk", dk, cfg.ldk, cfg.Hk), ("v", v, cfg.ldv, cfg.Hk), ("dv", dv, cfg.ldv, cfg.Hk)))
+    _need(f, dev, "dlam", dlam, _TORCH[cfg.dtype], cfg.H)
+    _need(f, dev, "ws", ws.ws, torch.uint8, 0)
+    _call(f, dev, stream, ctypes.byref(cfg), _p(dout), _p(q), _p(k), _p(v), _p(lam), _p(cu), _p(ws.saved),
+          ws.saved.numel(), _p(ws.ws), ws.ws.numel() if ws.ws is not None else 0, _p(dq), _p(dk), _p(dv), _p(dlam))
 
 
 def _name(t, what):
