@@ -50,6 +50,7 @@ template <bool REDO>
 __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                                    const __nv_bfloat16* v, __half* qs, __half* ks, __half* vs,
                                                    const DiffTile* tiles, const int* seq, uint32_t* amax, int* err) {
+  pdl_start();
   if ((int)blockIdx.x >= tiles[g.ntile].x) return;
   const int y = blockIdx.y;
   const int which = y < g.H ? kScaleQ : y < g.H + g.Hk ? kScaleK : kScaleV;
@@ -136,6 +137,7 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   const uint32_t sbase = smem_u32(sm);
   // long tiles of all heads first
   const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
+  pdl_start();
   if (rank >= tiles[g.ntile].x) return;                          // whole CTA, before any set-up
   const DiffTile t = tiles[rank];
   const int nkv = t.w + 1;
@@ -421,15 +423,12 @@ cudaError_t fwd_t(const DiffGeom& g, const DiffTC& b, const void* lam, void* o, 
     return cudaErrorInvalidValue;
   const int smem = FwdLayout<D>::BYTES;
   auto kern = k_diff_fwd_tc<D>;
-  cudaError_t e = diff_regs_ok(kern);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = diff_kernel_ready(done, (const void*)kern, smem);
   if (e != cudaSuccess) return e;
   const float c2 = (float)(1.4426950408889634 / sqrt((double)(D / 2)));
-  kern<<<g.ntile * g.H, kDiffThreads, smem, s>>>(tq, tk, tv, g, (const __nv_bfloat16*)lam, b.tiles, b.seq, b.amax,
-                                                (__nv_bfloat16*)o, train ? b.om : nullptr, train ? b.lse : nullptr, c2, err);
-  count_launch();
-  return cudaGetLastError();
+  return launch_next(kern, dim3(g.ntile * g.H), kDiffThreads, smem, s, tq, tk, tv, g, (const __nv_bfloat16*)lam, b.tiles,
+                     b.seq, b.amax, (__nv_bfloat16*)o, train ? b.om : nullptr, train ? b.lse : nullptr, c2, err);
 }
 
 }  // namespace
@@ -439,14 +438,11 @@ cudaError_t launch_diff_fwd_tc(const DiffGeom& g, const DiffTC& b, const void* q
   cudaError_t e = launch_diff_tiles(g, kDiffTileTC, b.tiles, b.seq, b.amax, err, s);
   if (e != cudaSuccess) return e;
   const dim3 grid(g.ntile, g.H + 2 * g.Hk);
-  k_diff_pack<false><<<grid, 256, 0, s>>>(g, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                                          b.qs, b.ks, b.vs, b.tiles, b.seq, b.amax, err);
-  count_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_pack<true><<<grid, 256, 0, s>>>(g, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                                         b.qs, b.ks, b.vs, b.tiles, b.seq, b.amax, err);
-  count_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  for (auto kern : {k_diff_pack<false>, k_diff_pack<true>}) {
+    e = launch_next(kern, grid, 256, 0, s, g, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, b.qs,
+                    b.ks, b.vs, b.tiles, b.seq, b.amax, err);
+    if (e != cudaSuccess) return e;
+  }
   return g.D == 64 ? fwd_t<64>(g, b, lam, o, train, err, s) : fwd_t<128>(g, b, lam, o, train, err, s);
 }
 

@@ -2,6 +2,8 @@
 // forward and backward kernels share.
 #pragma once
 
+#include <atomic>
+
 #include "k_diff.cuh"
 #include "tc_ptx.cuh"
 
@@ -39,15 +41,48 @@ __host__ __device__ __forceinline__ int diff_exp(uint32_t amax_bits) {
 // warpgroup of the producer and the issuer gives up 96 of them, each of the two
 // compute warpgroups takes 48 more: 72 + 2 * 216 = 3 * 168, so the split fits
 // the CTA's own allotment and no increase can wait for registers that never
-// come. diff_regs_ok makes sure of the 168 before the first launch.
+// come. diff_kernel_ready makes sure of the 168 before the first launch.
 constexpr int kDiffThreads = 384, kDiffLaunchRegs = 168;
 __device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
-template <typename K>
-cudaError_t diff_regs_ok(K kern) {
+// Checked and set once per kernel and device (the calls cost several us).
+// done: one bit per device, of one kernel.
+inline cudaError_t diff_kernel_ready(std::atomic<unsigned long long>& done, const void* kern, int smem) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load() >> dev & 1)) return cudaSuccess;
   cudaFuncAttributes a;
-  const cudaError_t e = cudaFuncGetAttributes(&a, kern);
-  return e != cudaSuccess ? e : a.numRegs == kDiffLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+  if ((e = cudaFuncGetAttributes(&a, kern)) != cudaSuccess) return e;
+  if (a.numRegs != kDiffLaunchRegs) return cudaErrorInvalidConfiguration;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  if (dev < 64) done.fetch_or(1ull << dev);
+  return cudaSuccess;
+}
+
+// Programmatic launch: the kernels of one pass follow each other closely (each
+// may be put on the GPU while the one before runs out). Every kernel of the
+// chain begins with pdl_start: it waits until the one before is done and its
+// writes are visible, before it touches memory. The first of a pass is launched
+// the ordinary way, behind everything in the stream.
+__device__ __forceinline__ void pdl_start() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&c, kern, args...);
 }
 
 // 16-wide slice i of a K-major tile's rows, as an offset of its descriptor

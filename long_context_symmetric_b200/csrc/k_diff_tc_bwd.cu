@@ -320,6 +320,7 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
   const int rank = (int)blockIdx.x % g.ntile, hk = (int)blockIdx.x / g.ntile;
+  pdl_start();
   if (rank >= tiles[g.ntile].x) return;
   if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
   const DiffTile tl = tiles[rank];
@@ -590,6 +591,7 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
   const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
+  pdl_start();
   if (rank >= tiles[g.ntile].x) return;
   if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
   const DiffTile tl = tiles[rank];
@@ -762,6 +764,7 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
   constexpr int L = D / 8, RPB = 256 / L;      // lanes per row, rows per step
   __shared__ float ws[8];
   const int h = blockIdx.y, hk = h / g.G, lane = threadIdx.x & 31;
+  if (REDO) pdl_start();
   if ((int)blockIdx.x >= tiles[g.ntile].x) {
     if (!REDO && threadIdx.x == 0) part[(size_t)h * g.ntile + blockIdx.x] = 0.f;
     return;
@@ -853,28 +856,25 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
       !make_tmap_16(&tv, b.vs, D, rows, g.Hk, true, 128) || !make_tmap_16(&tdo, b.dos, D, rows, g.H, true, 128))
     return cudaErrorInvalidValue;
   const int smem = BwdLayout<D, 2>::BYTES, smem_q = BwdLayout<D, 3>::BYTES;
-  cudaError_t e = diff_regs_ok(k_diff_dkdv_tc<D>);
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = diff_kernel_ready(done[0], (const void*)k_diff_dkdv_tc<D>, smem);
   if (e != cudaSuccess) return e;
-  if ((e = diff_regs_ok(k_diff_dq_tc<D>)) != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_diff_dkdv_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_diff_dq_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
-  if (e != cudaSuccess) return e;
+  if ((e = diff_kernel_ready(done[1], (const void*)k_diff_dq_tc<D>, smem_q)) != cudaSuccess) return e;
   const float scale = (float)(1.0 / sqrt((double)(D / 2)));
   const float c2 = (float)(1.4426950408889634 / sqrt((double)(D / 2)));
   const dim3 gp(g.ntile, g.H);
   const __nv_bfloat16 *L = (const __nv_bfloat16*)lam, *dO = (const __nv_bfloat16*)dout;
   k_diff_pack_do<false, D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta, b.part, err);
+  count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_pack_do<true, D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta, b.part, err);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_dkdv_tc<D><<<g.ntile * g.Hk, kDiffThreads, smem, s>>>(tk, tv, tq, tdo, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
-                                                           b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  k_diff_dq_tc<D><<<g.ntile * g.H, kDiffThreads, smem_q, s>>>(tq, tdo, tk, tv, g, L, b.tiles, b.seq, b.amax, b.amax_do, b.lse,
-                                                        b.delta, (__nv_bfloat16*)dq, c2, scale, err);
-  count_launch(4);
-  return cudaGetLastError();
+  e = launch_next(k_diff_pack_do<true, D>, gp, 256, 0, s, g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta,
+                  b.part, err);
+  if (e != cudaSuccess) return e;
+  e = launch_next(k_diff_dkdv_tc<D>, dim3(g.ntile * g.Hk), kDiffThreads, smem, s, tk, tv, tq, tdo, g, L, b.tiles, b.seq,
+                  b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
+  if (e != cudaSuccess) return e;
+  return launch_next(k_diff_dq_tc<D>, dim3(g.ntile * g.H), kDiffThreads, smem_q, s, tq, tdo, tk, tv, g, L, b.tiles, b.seq,
+                     b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dq, c2, scale, err);
 }
 
 }  // namespace
