@@ -392,7 +392,8 @@ lh_status lh_cp_spread(const lh_config* cfg, int world, int rank, const float* d
  * nothing between calls: two calls may run at the same time as long as each
  * has its own outputs and its own workspace (that holds for the replays of two
  * captured graphs too). Inputs and outputs do not overlap, except where an
- * entry point says so.
+ * entry point says so. Row statistics (mean, rstd) and positions need the
+ * alignment of their own elements only, so that a range of tokens can be passed.
  * ------------------------------------------------------------------------- */
 
 /* Layer norm of M rows of d values:

@@ -548,10 +548,10 @@ cudaError_t launch_norm_fwd(const lh_norm_config& c, const void* x, const void* 
   a.M = c.M; a.ldx = c.ldx ? c.ldx : c.d; a.ldy = c.ldy ? c.ldy : c.d; a.d = c.d;
   a.wbf16 = c.wdtype == LH_BF16; a.eps = c.eps; a.inv_d = 1.f / (float)c.d;
   const bool vec = norm_vec(c, a.ldx, a.ldy);
-  // a warp per row where there are rows enough to fill the GPU with warps:
-  // 98,304 rows of 2,048: 150 us against 171 with a block per row; 64 rows of
-  // 1,024: 7.2 against 4.8
-  const NormShape s = norm_shape(c.d, vec && c.dtype == LH_BF16 && c.M >= 16 * kNormSMs);
+  // a warp per row of up to 2,048 bf16 values: 98,304 rows of 2,048 take 150 us
+  // against 171 with a block per row; 64 rows of 1,024 take 7.2 against 4.8 (from
+  // cold), but by the row count one row would have other bits in another batch
+  const NormShape s = norm_shape(c.d, vec && c.dtype == LH_BF16);
   if (c.dtype == LH_BF16)
     return vec ? fwd_t<__nv_bfloat16, true>(s, a, st) : fwd_t<__nv_bfloat16, false>(s, a, st);
   return vec ? fwd_t<float, true>(s, a, st) : fwd_t<float, false>(s, a, st);

@@ -562,6 +562,8 @@ lh_status check_norm(const lh_norm_config* c) {
   return LH_OK;
 }
 #define LH_OPT(p) do { if (!aligned16(p)) return LH_ERR_ALIGN; } while (0)
+// per-row or per-token values, read and written one by one: their own size
+#define LH_ELEM(p, size) do { if ((uintptr_t)(p) & ((size) - 1)) return LH_ERR_ALIGN; } while (0)
 }  // namespace
 
 lh_status lh_norm_plan(const lh_norm_config* cfg, size_t* ws_bytes) {
@@ -577,7 +579,7 @@ lh_status lh_norm_fwd(const lh_norm_config* cfg, const void* x, const void* w, c
   lh_status st = check_norm(cfg);
   if (st != LH_OK) return st;
   if (cfg->M == 0) return LH_OK;
-  LH_REQ(x); LH_REQ(y); LH_OPT(w); LH_OPT(b); LH_OPT(mean); LH_OPT(rstd);
+  LH_REQ(x); LH_REQ(y); LH_OPT(w); LH_OPT(b); LH_ELEM(mean, 4); LH_ELEM(rstd, 4);
   LH_CUDA(launch_norm_fwd(*cfg, x, w, b, y, mean, rstd, (cudaStream_t)stream));
   return LH_OK;
 }
@@ -589,7 +591,9 @@ lh_status lh_norm_bwd(const lh_norm_config* cfg, const void* dy, const void* x, 
   if (st != LH_OK) return st;
   LH_OPT(w); LH_OPT(dw); LH_OPT(db);
   if (cfg->M > 0) {
-    LH_REQ(dy); LH_REQ(x); LH_REQ(mean); LH_REQ(rstd); LH_REQ(dx);
+    LH_REQ(dy); LH_REQ(x); LH_REQ(dx);
+    if (!mean || !rstd) return LH_ERR_NULL;
+    LH_ELEM(mean, 4); LH_ELEM(rstd, 4);
     if (dw || db) {
       LH_REQ(ws);
       if (ws_bytes < norm_ws_bytes(*cfg)) return LH_ERR_WORKSPACE;
@@ -619,7 +623,9 @@ lh_status lh_rope(const lh_rope_config* c, const void* q, const void* k, const v
   for (long long s : {c->q_bs, c->k_bs, c->qo_bs, c->ko_bs, c->pos_as, c->pos_bs})
     if (s < 0 || s > (1LL << 44)) return LH_ERR_SHAPE;
   if ((long long)c->B * c->N == 0) return LH_OK;
-  LH_REQ(q); LH_REQ(qo); LH_REQ(pos); LH_REQ(freq); LH_REQ(axis);
+  LH_REQ(q); LH_REQ(qo); LH_REQ(freq); LH_REQ(axis);
+  if (!pos) return LH_ERR_NULL;
+  LH_ELEM(pos, c->pos64 ? 8 : 4);
   if (c->Hk) { LH_REQ(k); LH_REQ(ko); }
   int* err = device_error_ptr();
   if (!err) return LH_ERR_CUDA;

@@ -17,6 +17,12 @@ into chunks of whole coarsest blocks small enough to stay in the 126 MB L2:
                      Y = O W_o (on two streams in turn), reading chunk i of O
                      from L2 while chunk i+1 is being scattered.
 
+In front of the pool a layer usually normalises its input and rotates its
+queries and keys by their positions. ``qkv_project_pool`` takes both along
+(``norm``, ``rope``), chunk by chunk too: a chunk's rows are normalised right
+before its projections read them, its queries and keys rotated in place right
+before the pool reads them.
+
 The projections are plain library GEMMs (they are the model's, not the path's);
 every step of the path stays a liblh kernel. The pool and scatter results
 are bit-identical to lh_pool and lh_scatter over the whole sequence. A 512K
@@ -27,11 +33,33 @@ and replays it.
 
 from __future__ import annotations
 
+from dataclasses import dataclass
+
 import torch
 
 from . import lh
 
-__all__ = ["chunk_tokens", "qkv_project_pool", "scatter_project", "Graphed"]
+__all__ = ["chunk_tokens", "InputNorm", "Positions", "qkv_project_pool", "scatter_project", "Graphed"]
+
+
+@dataclass
+class InputNorm:
+    """Layer norm of the input rows: w and b [d_model] (either None), and what the pass leaves for its backward:
+    the normalised rows xn [B, N, d_model] (x's type), mean and rstd [B, N] (fp32)."""
+    w: torch.Tensor | None
+    b: torch.Tensor | None
+    xn: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    eps: float = 1e-5
+
+
+@dataclass
+class Positions:
+    """Rotary positions of the queries and keys: pos [axes, B, N] (int32 or int64) and the plan's tables."""
+    pos: torch.Tensor
+    plan: lh.RopePlan
+    pairs: str = "half"
 
 
 def chunk_tokens(cfg, target: int = 8192) -> int:
@@ -47,12 +75,16 @@ def _streams(n, given):
     return list(given) if given is not None else [torch.cuda.Stream() for _ in range(n)]
 
 
-def qkv_project_pool(cfg, ws, x, w_q, w_k, w_v, q, k, v, chunk=None, side=None, gemm_streams=None):
+def qkv_project_pool(cfg, ws, x, w_q, w_k, w_v, q, k, v, chunk=None, side=None, gemm_streams=None,
+                     norm: InputNorm | None = None, rope: Positions | None = None):
     """q, k, v [B, N, H, D] = x [B, N, d_model] @ w_* [d_model, H*D], and the
     pyramid / norms of ws (lh.Workspace) by lh_pool_range, chunk by chunk.
     A chunk's three projections run at once (the current stream and two of
     `gemm_streams`), so that together they fill the GPU; the pool of chunk i
-    runs on `side` once all three have written it."""
+    runs on `side` once all three have written it. With `norm` the projections
+    read the layer norm of x (lh_norm_fwd); with `rope` q and k are rotated
+    (lh_rope) before they are pooled. Both give the same bits as the calls over
+    the whole sequence."""
     B, N = cfg.B, cfg.N
     HD = cfg.H * cfg.D
     c = chunk or chunk_tokens(cfg)
@@ -61,14 +93,37 @@ def qkv_project_pool(cfg, ws, x, w_q, w_k, w_v, q, k, v, chunk=None, side=None, 
     gs = [main] + _streams(2, gemm_streams)
     for st in gs[1:] + [side]:
         st.wait_stream(main)
+    dtype = {lh.LH_BF16: "bf16", lh.LH_FP32: "fp32"}[cfg.dtype]
+    if norm is not None:
+        p = norm.w if norm.w is not None else norm.b
+        ncfg = lh.make_norm_config(c, x.shape[-1], dtype, dtype if p is None else lh.type_name(p, "InputNorm"), norm.eps)
+    if rope is not None:
+        pos = rope.pos
+        if tuple(pos.shape) != (rope.plan.axes, B, N) or not pos.is_contiguous():
+            raise ValueError(f"qkv_project_pool: positions of shape {tuple(pos.shape)}, ({rope.plan.axes}, {B}, {N}) contiguous ones are wanted")
+        bs = N * HD
+        rcfg = lh.make_rope_config(B, c, cfg.H, cfg.H, cfg.D, rope.plan.rot, rope.plan.axes, dtype, rope.pairs,
+                                   pos64=pos.dtype == torch.int64, q_bs=bs, k_bs=bs, qo_bs=bs, ko_bs=bs, pos_as=B * N, pos_bs=N)
+    src = x if norm is None else norm.xn
     for t0 in range(0, N, c):
+        if norm is not None:
+            for b in range(B):
+                lh.norm_fwd(ncfg, x[b, t0:t0 + c], norm.w, norm.b, norm.xn[b, t0:t0 + c], norm.mean[b, t0:t0 + c],
+                            norm.rstd[b, t0:t0 + c], stream=main)
+            ev = torch.cuda.Event()
+            ev.record(main)
+            for st in gs[1:]:
+                st.wait_event(ev)
         for (w, out), st in zip(((w_q, q), (w_k, k), (w_v, v)), gs):
             with torch.cuda.stream(st):
                 for b in range(B):
-                    torch.matmul(x[b, t0:t0 + c], w, out=out[b, t0:t0 + c].view(c, HD))
+                    torch.matmul(src[b, t0:t0 + c], w, out=out[b, t0:t0 + c].view(c, HD))
             ev = torch.cuda.Event()
             ev.record(st)
             side.wait_event(ev)
+        if rope is not None:
+            qc, kc = q[:, t0:t0 + c], k[:, t0:t0 + c]
+            lh.rope(rcfg, qc, kc, pos[:, :, t0:], rope.plan.freq, rope.plan.axis, qc, kc, stream=side)
         lh.pool_range(cfg, t0, c, q, k, v, ws.pyr_q, ws.pyr_k, ws.pyr_v, ws.sq, ws.scale, stream=side)
     for st in gs[1:] + [side]:
         main.wait_stream(st)

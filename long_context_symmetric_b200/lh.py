@@ -600,7 +600,8 @@ def diff_attn_bwd(cfg, dout, q, k, v, lam, ws: DiffWorkspace, dq, dk, dv, dlam, 
           ws.saved.numel(), _p(ws.ws), ws.ws.numel() if ws.ws is not None else 0, _p(dq), _p(dk), _p(dv), _p(dlam))
 
 
-def _name(t, what):
+def type_name(t, what):
+    """The library's name of a tensor's type."""
     if t.dtype not in _NAMES:
         raise ValueError(f"{what}: {t.dtype} is not supported (bfloat16, float32)")
     return _NAMES[t.dtype]
@@ -627,7 +628,7 @@ class LayerNorm(torch.autograd.Function):
         w, b = (None if t is None else _whole(t) for t in (w, b))
         p = w if w is not None else b
         M = x.numel() // d if d else 0
-        cfg = make_norm_config(M, d, _name(x, "layer_norm"), _name(x if p is None else p, "layer_norm"), eps)
+        cfg = make_norm_config(M, d, type_name(x, "layer_norm"), type_name(x if p is None else p, "layer_norm"), eps)
         y = torch.empty_like(x)
         mean, rstd = (torch.empty(M, dtype=torch.float32, device=x.device) for _ in range(2))
         norm_fwd(cfg, x, w, b, y, mean, rstd)
@@ -708,7 +709,7 @@ class Rotary(torch.autograd.Function):
         if k.shape[:2] != (B, N) or k.shape[3] != D or k.dtype != q.dtype:
             raise ValueError(f"rotary: q {tuple(q.shape)} {q.dtype} and k {tuple(k.shape)} {k.dtype} do not belong together")
         q, k, pos = _whole(q), _whole(k), plan.positions(pos, B, N)
-        cfg = make_rope_config(B, N, H, k.shape[2], D, plan.rot, plan.axes, _name(q, "rotary"), pairs,
+        cfg = make_rope_config(B, N, H, k.shape[2], D, plan.rot, plan.axes, type_name(q, "rotary"), pairs,
                                pos64=pos.dtype == torch.int64, shared_pos=pos.ndim == 2)
         qo, ko = torch.empty_like(q), torch.empty_like(k)
         rope(cfg, q, k, pos, plan.freq, plan.axis, qo, ko)
@@ -743,7 +744,7 @@ class DifferentialAttention(torch.autograd.Function):
         if any(t.dtype != q.dtype for t in (k, v, lam)) or tuple(lam.shape) != (H,):
             raise ValueError("differential_attention: k, v and lam [H] have q's type")
         q, k, v, lam = (_whole(t) for t in (q, k, v, lam))
-        name = _name(q, "differential_attention")
+        name = type_name(q, "differential_attention")
         cfg = (make_diff_config(cu.numel() - 1, 0, H, D, name, Hk, rows=q.shape[0]) if packed
                else make_diff_config(q.shape[0], q.shape[1], H, D, name, Hk))
         ws = DiffWorkspace(cfg, q.device)
