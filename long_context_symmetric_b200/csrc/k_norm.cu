@@ -462,10 +462,12 @@ NormShape norm_shape(int d, bool warp_rows) {
   return {0, (th + 31) / 32 * 32, nv};
 }
 constexpr int kNormSMs = 148;
-// Resident blocks: 1,024 threads to an SM (about 64 registers each).
+// Resident blocks: as many as the registers allow, 1,024 threads to an SM for rows
+// that lanes of a warp hold, 512 for rows that a block holds.
 int norm_blocks(const NormShape& s, long long M, int R) {
   const long long groups = s.G ? s.threads / s.G : 1, need = (M + groups * R - 1) / (groups * R);
-  const long long most = (long long)kNormSMs * (1024 / s.threads < 1 ? 1 : 1024 / s.threads);
+  const int per_sm = (s.G ? 1024 : 512) / s.threads;
+  const long long most = (long long)kNormSMs * (per_sm < 1 ? 1 : per_sm);
   return (int)(need < most ? need : most);
 }
 constexpr int kRF = 2;               // rows in flight per group, forward pass (nv = 1)
