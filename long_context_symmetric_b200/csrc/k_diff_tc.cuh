@@ -23,7 +23,7 @@ struct DiffTC {
   uint32_t* amax_do;          // [B][Hk], like q's
   __half* dos;                // [H][padded rows][D]
   float* delta;               // [H][2][padded rows]
-  float* part;                // [H][ntile] sums of delta 2
+  float* part;                // [H][ntile] sums of A2 dP
 };
 
 // The power of two of a working copy: x 2^-e, e = 0 while the head's largest

@@ -13,8 +13,10 @@
 // dS leaves fp16 whatever the data, and an average one (A of 1 / n) stays
 // normal. The powers are taken out of the fp32 results.
 //
-// k_diff_pack_do copies do like the forward's working copies and forms d1, d2
-// (and per tile the sum of d2) in the same pass.
+// k_diff_pack_do copies do like the forward's working copies and forms d1, d2 in
+// the same pass. (The sum of d2 that dlam needs is formed as the sum of A2 dP in
+// the dq kernel, from fp32 values: a sum over a long sequence can be small beside
+// its terms, and the saved outputs' 11 bits would show in it.)
 //
 // k_diff_dkdv_tc: one CTA per key tile and key/value head, over the query tiles
 // from its own on, of every query head that shares it. Work per pair of tiles:
@@ -24,12 +26,18 @@
 // columns, once dP is in registers, take the operands: each 32-column chunk
 // holds dS_1 (then dS_2, once dK_1 has read it) in its first 16 and A1 (then A1 -
 // lam A2) in its last 16. Order of the products:
-//   X_1(t+1) | X_2(t), dK_1(t), dV(t), dK_2(t), Y(t+1)
+//   X_2(t), dK_1(t), X_1(t+1), dV(t), dK_2(t), Y(t+1)
+// A warp of its own brings the queries' statistics, three tiles ahead.
 // k_diff_dq_tc: one CTA per query tile and head, over the key tiles up to its
 // own: X_1, X_2, Y, dQ_1, dQ_2, TMEM X_1 | X_2 | Y | dQ. Both scores of tile t+1
 // run under the exponentials of tile t, dQ(t) and Y(t+1) under those of t+1.
 // 32,768 exponentials per pair in each kernel: 2,048 cycles of the special-
-// function unit against 2,048 (dk, dv) and 1,536 (dq) tensor cycles.
+// function unit against 2,048 (dk, dv) and 1,536 (dq) tensor cycles. Measured at 16
+// heads of 8,192 tokens, D = 128: 665 and 445 us, 5,100 and 3,300 cycles per pair:
+// the two warpgroups exponentiate (1,050 cycles per map) and multiply (470 .. 700)
+// at the same time, so the two pipes take turns. Giving each warpgroup its own
+// 64-column halves, half a tile apart, was slower (1,000 and 800 us): score products
+// of N = 64 and twice as many of them.
 #include "k_diff_tc.cuh"
 
 namespace lh {
@@ -585,14 +593,19 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
              const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DiffGeom g,
              const __nv_bfloat16* __restrict__ lam, const DiffTile* __restrict__ tiles, const int* __restrict__ seq,
              const uint32_t* __restrict__ amax, const uint32_t* __restrict__ amax_do, const float* __restrict__ lse,
-             const float* __restrict__ delta, __nv_bfloat16* __restrict__ dq, float c2, float scale, int* err) {
+             const float* __restrict__ delta, __nv_bfloat16* __restrict__ dq, float* __restrict__ part, float c2, float scale,
+             int* err) {
   using Lay = BwdLayout<D, 3>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
+  float* red = reinterpret_cast<float*>(smem_raw + 256);          // the compute warps' sums of A2 dP
   const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
   pdl_start();
-  if (rank >= tiles[g.ntile].x) return;
+  if (rank >= tiles[g.ntile].x) {
+    if (threadIdx.x == 0) part[(size_t)h * g.ntile + rank] = 0.f;
+    return;
+  }
   if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
   const DiffTile tl = tiles[rank];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -662,6 +675,7 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     const float nl1 = in ? (float)pw.sp - lse[at] : 0.f, nl2 = in ? (float)pw.sp - lse[at + rows] : 0.f;
     const float nd1 = in ? delta[at] * md : 0.f, nd2 = in ? delta[at + rows] * md : 0.f;
     c2 *= pow2f(pw.eq + pw.ek);
+    float2 dl = make_float2(0.f, 0.f);                    // sum of A2 dP of this thread's columns
     bool ok = true;
     for (int t = 0; t < n; ++t) {
       uint32_t a0[32], a1[32], b0[32], b1[32];
@@ -701,26 +715,31 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
       const uint32_t cY = cX + kQY;
       const float2 ff = make_float2(f, f), v1 = make_float2(nd1, nd1), v2 = make_float2(nd2, nd2);
       // 16 columns of dP, then both maps' dS (8 packed columns each) into them
-      auto part = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], int o, uint32_t at16) {
+      auto cols16 = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], int o, uint32_t at16) {
         uint32_t d[16], pk[16];
         tmem_ld16(at16, d);
         tmem_wait_ld_regs16(d);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float2 dd = f2(d[e], d[e + 1]);
+          dl = __ffma2_rn(f2(b[o + e], b[o + e + 1]), dd, dl);
           pk[e >> 1] = h2_bits(__float22half2_rn(__fmul2_rn(f2(a[o + e], a[o + e + 1]), __ffma2_rn(dd, ff, v1))));
           pk[8 + (e >> 1)] = h2_bits(__float22half2_rn(__fmul2_rn(f2(b[o + e], b[o + e + 1]), __ffma2_rn(dd, ff, v2))));
         }
         tmem_st16(at16, pk);
       };
-      part(a0, b0, 0, cY);
-      part(a0, b0, 16, cY + 16);
-      part(a1, b1, 0, cY + 32);
-      part(a1, b1, 16, cY + 48);
+      cols16(a0, b0, 0, cY);
+      cols16(a0, b0, 16, cY + 16);
+      cols16(a1, b1, 0, cY + 32);
+      cols16(a1, b1, 16, cY + 48);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_warp(&bars->ds_ready);
     }
+    float d2 = (dl.x + dl.y) * pow2f(pw.edo + pw.ev) * pow2f(-pw.sp);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) d2 += __shfl_xor_sync(0xffffffffu, d2, o);
+    if (lane == 0) red[warp - 4] = d2;
     if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->done, 0, ab, err, 51))) {
       tc_fence_after();
       // dS_2 goes without its factor -lam until here (half 1 holds map 2's columns)
@@ -750,6 +769,11 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     }
   }
   bwd_teardown(tbase, warp);
+  if (threadIdx.x == 0) {
+    float d2 = 0.f;
+    for (int w = 0; w < kComputeWarps; ++w) d2 += red[w];
+    part[(size_t)h * g.ntile + rank] = d2;
+  }
 }
 
 // ---------------------------------------------------------------- do: working copy, d1, d2
@@ -760,15 +784,11 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
                                                       const __half* __restrict__ om, const DiffTile* __restrict__ tiles,
                                                       const int* __restrict__ seq, const uint32_t* __restrict__ amax,
                                                       uint32_t* amax_do, __half* __restrict__ dos,
-                                                      float* __restrict__ delta, float* __restrict__ part, int* err) {
+                                                      float* __restrict__ delta, int* err) {
   constexpr int L = D / 8, RPB = 256 / L;      // lanes per row, rows per step
-  __shared__ float ws[8];
   const int h = blockIdx.y, hk = h / g.G, lane = threadIdx.x & 31;
   if (REDO) pdl_start();
-  if ((int)blockIdx.x >= tiles[g.ntile].x) {
-    if (!REDO && threadIdx.x == 0) part[(size_t)h * g.ntile + blockIdx.x] = 0.f;
-    return;
-  }
+  if ((int)blockIdx.x >= tiles[g.ntile].x) return;
   const DiffTile t = tiles[blockIdx.x];
   const size_t sh = (size_t)seq[blockIdx.x] * g.Hk + hk;
   float mul = 1.f;
@@ -781,7 +801,6 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
   const size_t rows = (size_t)g.ntile * 128;
   const float pv = REDO ? 1.f : pow2f(diff_exp(amax[(size_t)kScaleV * g.B * g.Hk + sh]));
   uint32_t mx = 0;
-  float tot = 0.f;
 #pragma unroll 2
   for (int r = threadIdx.x / L; r < 128; r += RPB) {
     const bool in = r0 + r < t.y;
@@ -817,7 +836,6 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
       if (threadIdx.x % L == 0) {
         delta[(size_t)h * 2 * rows + prow] = a * pv;
         delta[(size_t)(h * 2 + 1) * rows + prow] = b * pv;
-        tot += b * pv;
       }
     }
     uint4 out;
@@ -829,21 +847,9 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
   if (!REDO) {
     const bool fin = mx < 0x7F800000u;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    }
-    if (lane == 0) {
-      if (mx > amax_do[sh]) atomicMax(amax_do + sh, mx);
-      ws[threadIdx.x >> 5] = tot;
-    }
+    for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0 && mx > amax_do[sh]) atomicMax(amax_do + sh, mx);
     if (!fin) report_error(err, LH_ERR_DEVICE, 102);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float s = 0.f;
-      for (int i = 0; i < 8; ++i) s += ws[i];
-      part[(size_t)h * g.ntile + blockIdx.x] = s;
-    }
   }
 }
 
@@ -864,17 +870,17 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
   const float c2 = (float)(1.4426950408889634 / sqrt((double)(D / 2)));
   const dim3 gp(g.ntile, g.H);
   const __nv_bfloat16 *L = (const __nv_bfloat16*)lam, *dO = (const __nv_bfloat16*)dout;
-  k_diff_pack_do<false, D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta, b.part, err);
+  k_diff_pack_do<false, D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta, err);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_next(k_diff_pack_do<true, D>, gp, 256, 0, s, g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta,
-                  b.part, err);
+                  err);
   if (e != cudaSuccess) return e;
   e = launch_next(k_diff_dkdv_tc<D>, dim3(g.ntile * g.Hk), kDiffThreads, smem, s, tk, tv, tq, tdo, g, L, b.tiles, b.seq,
                   b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
   if (e != cudaSuccess) return e;
   return launch_next(k_diff_dq_tc<D>, dim3(g.ntile * g.H), kDiffThreads, smem_q, s, tq, tdo, tk, tv, g, L, b.tiles, b.seq,
-                     b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dq, c2, scale, err);
+                     b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dq, b.part, c2, scale, err);
 }
 
 }  // namespace

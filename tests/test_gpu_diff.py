@@ -229,3 +229,30 @@ def test_autograd_and_differences():
     assert torch.equal(o2.view_as(o), o)
     for a, b in zip(leaves, packed):
         assert torch.equal(a.grad.view_as(b.grad), b.grad)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_dlam_of_a_sum_that_cancels(dtype):
+    """dlam is a sum over all rows that can be small beside its terms. Its terms are A2 dP, kept in fp32, so its error
+    counts fp32 roundings of the sum of the magnitudes (of which a thread adds n/2 and the rest goes by trees), and a
+    single rounding of the result."""
+    N, D = 3000, 128
+    q, k, v, lam, do = inputs(111, N, 1, 1, D, dtype)
+    Q, K, V, G = (t[:, 0].double() for t in (q, k, v, do))
+    late = torch.ones(N, N, dtype=torch.bool, device=DEV).triu(1)
+    a2 = (Q[:, 64:] @ K[:, 64:].T / 8).masked_fill(late, -torch.inf).softmax(-1)
+    terms = a2 * (G @ V.T)
+    mag = a2 * (G.abs() @ V.abs().T)
+    # the part of do along a2 v that makes the sum nearly vanish is taken out
+    o2 = a2 @ V
+    do2 = (G - (terms.sum() / (o2 * o2).sum()) * o2).to(DT[dtype]).view(N, 1, D)
+    want = -(do2[:, 0].double() * o2).sum()
+    cfg = lh.make_diff_config(1, N, 1, D, dtype)
+    got = run(cfg, q, k, v, lam, do2)["dlam"].double()
+    U = 2.0 ** -24
+    # scores of 64 products, scale and exponent: 2 (64 + 4) U |s| <= 2 * 68 * 16 U relative, the exponential 2^-21, the
+    # products and sums of dP 136 U, the sum over columns (N / 2 + 64) U; statistically independent, so their root mean
+    # square over the terms carries into the sum: sqrt(sum of squares) times 8 covers it
+    rel = (2 * 68 * 16 + 136 + 64 + 2 ** 3) * U + 2.0 ** -21
+    tol = 8 * rel * float(mag.square().sum().sqrt()) + (N / 2 + 64) * U * float(terms.abs().sum()) / N ** 0.5
+    assert abs(float(got - want)) <= tol + HALF[dtype] * abs(float(want)), (float(got), float(want), tol)
