@@ -24,7 +24,7 @@
 // takes every r-th tile of the walk, leaves its sums in its shared memory, and
 // each block adds up an equal share of the rows from all of them, in rank order
 // (forward pass: after scaling to the common maximum). 1,021 tokens of 4 heads of
-// 64, forward and backward: 464 us without.
+// 64, forward and backward: 464 us without, 242 us with.
 #include <cooperative_groups.h>
 
 #include "k_diff.cuh"

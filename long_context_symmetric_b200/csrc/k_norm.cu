@@ -10,16 +10,23 @@
 // memory), so a row whose mean is far above its deviation keeps its digits.
 //
 // Bound by HBM: x is read and y written once; the backward reads x and dy and
-// writes dx once. A row is held in registers by a group of threads, 8 values
-// each: G = 4 .. 32 lanes of a warp for rows of up to 256 values (several rows
-// to a warp, sums by shuffles alone), a whole block for longer rows (one
-// barrier per reduction, the partial sums alternating between two buffers).
-// Blocks stay resident and walk the rows with a stride, R rows at a time, so
-// that the weights are loaded once and R rows' loads are in flight together;
-// the backward keeps its columns' dw and db in registers (in shared memory for
-// rows of more than 8,192 values, where 512 threads hold 32 columns each and
+// writes dx once. A row is held in registers by a group of threads, 8 values to
+// a vector: G = 4 .. 32 lanes of a warp for rows of up to 256 values (several rows
+// to a warp, sums by shuffles alone), a block for longer ones (one barrier per
+// reduction, the partial sums alternating between two buffers); the forward pass
+// of bf16 rows of up to 2,048 values takes a warp per row, with no barrier. The
+// blocks, but for those, stay resident and walk the rows with a stride, R rows at
+// a time and the next R on their way meanwhile, so that the weights are loaded
+// once; the backward keeps its columns' dw and db in registers (in shared memory
+// for rows of more than 8,192 values, where 512 threads hold 32 columns each and
 // the registers do not suffice) and writes one partial row per block, which a
-// second kernel adds in a fixed order: no atomics, the same bits every run.
+// second kernel adds in a fixed order: no atomics, the same bits every run. Which
+// form a row takes goes by its length, type and alignment, never by the number of
+// rows, so a row has the same bits in any batch. Arithmetic goes in packed pairs.
+//
+// Measured: 98,304 rows of 2,048 bf16 148 us forward (5.4 TB/s), 222 us backward
+// (5.4), 4 us the sums; 1,048,576 of 128 96 us (5.6) and 133 us (6.1); 5,003 of 1,537
+// fp32 19 and 33 us.
 //
 // Rows of odd length, or whose stride is no multiple of 8 elements, are read
 // element by element with the columns dealt out to neighbouring lanes (VEC =
