@@ -394,6 +394,8 @@ lh_status lh_cp_spread(const lh_config* cfg, int world, int rank, const float* d
  * captured graphs too). Inputs and outputs do not overlap, except where an
  * entry point says so. Row statistics (mean, rstd) and positions need the
  * alignment of their own elements only, so that a range of tokens can be passed.
+ * Make the first call of each entry point on a device before any stream capture
+ * (it looks up the device error word and sets kernel attributes).
  * ------------------------------------------------------------------------- */
 
 /* Layer norm of M rows of d values:
@@ -468,9 +470,10 @@ lh_status lh_rope(const lh_rope_config* cfg, const void* q, const void* k, const
  *   o = A1 v - lam A2 v,  A_m = softmax(q_m k_m^T / sqrt(D/2) + causal mask).
  * Query head h reads key/value head h / (H / Hk). */
 typedef struct {
-  int B;                     /* sequences, >= 1 */
+  int B;                     /* sequences, 1 .. 65,536 */
   int T;                     /* token rows of q, k, v, o in all, >= 0, < 2^30 */
-  int H, Hk, D;              /* query heads, key/value heads (Hk divides H), D in {64, 128} */
+  int H, Hk, D;              /* query heads, key/value heads (Hk divides H), D in {64, 128};
+                                H + 2 Hk < 2^16, H (T / 64 + B + 1) < 2^31 */
   lh_dtype dtype;            /* q, k, v, lam, o and the gradients */
   int packed;                /* 0: B sequences of T / B rows each (B divides T); 1: `cu` gives them */
   int train;                 /* keep what lh_diff_attn_bwd needs */
@@ -495,13 +498,16 @@ lh_status lh_diff_plan(const lh_diff_config* cfg, lh_diff_plan_t* out);
  * read nor written, and a sequence's rows are read for that sequence alone.
  * packed = 0: cu is NULL. bf16 I/O runs on the tensor cores (fp16 operands
  * with a power of two per sequence and head, as in lh_attn_fwd; a non-finite
- * value is reported, LH_ERR_DEVICE detail 102), fp32 in fp32 arithmetic. */
+ * value is reported, LH_ERR_DEVICE detail 102), fp32 in fp32 arithmetic. A
+ * non-finite k or v value may reach every row of its sequence and head (0 times
+ * it is not 0), no other. */
 lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void* k, const void* v, const void* lam,
                            const int32_t* cu, void* o, void* saved, size_t saved_bytes, void* stream);
 
 /* Gradients of lh_diff_attn_fwd (cfg->train = 1, same cfg, inputs and
- * saved): dq, dk, dv (rows outside the sequences are not written) and
- * dlam [H]. Deterministic, shared heads included (no atomics). */
+ * saved; a buffer that no forward pass of this problem wrote is reported,
+ * LH_ERR_DEVICE detail 404, and not followed): dq, dk, dv (rows outside the
+ * sequences are not written) and dlam [H]. Deterministic, shared heads included (no atomics). */
 lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const void* q, const void* k, const void* v,
                            const void* lam, const int32_t* cu, const void* saved, size_t saved_bytes,
                            void* ws, size_t ws_bytes, void* dq, void* dk, void* dv, void* dlam, void* stream);

@@ -25,17 +25,21 @@ __global__ void k_diff_tiles(const DiffGeom g, int ts, DiffTile* tiles, int* seq
     for (int i = threadIdx.x; i < 3 * g.Hk; i += blockDim.x) amax[((size_t)(i / g.Hk) * g.B + b) * g.Hk + i % g.Hk] = 0;
   const int n = (hi - lo + ts - 1) / ts;
   const int pad = (lo + ts - 1) / ts * ts + b * ts;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+  // a warp per tile, its lanes over the sequences
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += blockDim.x >> 5) {
     long long rank = 0;
     if (g.cu) {
-      for (int c = 0; c < g.B; ++c) {
+      for (int c = lane; c < g.B; c += 32) {
         const int m = seq_tiles(g, c, ts);
         rank += max(0, m - 1 - i) + (c < b && m > i ? 1 : 0);
       }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     } else {
       rank = (long long)g.B * (n - 1 - i) + b;
     }
-    if (rank < g.ntile) {
+    if (lane == 0 && rank < g.ntile) {
       tiles[rank] = make_int4(lo, hi - lo, pad, i);
       if (seq) seq[rank] = b;
     }
@@ -48,7 +52,7 @@ __global__ void k_diff_tiles(const DiffGeom g, int ts, DiffTile* tiles, int* seq
     for (int c = threadIdx.x; c < g.B; c += blockDim.x) s += seq_tiles(g, c, ts);
     atomicAdd(&total, s);
     __syncthreads();
-    if (threadIdx.x == 0) tiles[g.ntile] = make_int4(min(total, g.ntile), 0, 0, 0);
+    if (threadIdx.x == 0) tiles[g.ntile] = make_int4(min(total, g.ntile), g.tag, 0, 0);
   }
 }
 

@@ -24,16 +24,28 @@ struct DiffGeom {
   long long ldq, ldk, ldv, ldo;   // elements between token rows
   const int* cu;                  // device offsets [B + 1], or NULL
   int ntile;                      // entries of the tile table
+  int tag;                        // of the problem that the tile table belongs to
 };
 
 // One entry: first row, rows, padded first row, tile index within the sequence.
-// tiles[ntile].x holds the number of entries that are in use.
+// tiles[ntile] holds the number of entries that are in use and the problem's tag.
 using DiffTile = int4;
+
+// Entries in use; none (and a report) where the buffer was not written for this
+// problem, so that no kernel follows a table of something else.
+__device__ __forceinline__ int diff_used(const DiffTile* tiles, const DiffGeom& g, int* err) {
+  const int4 t = tiles[g.ntile];
+  if (t.y == g.tag) return t.x;
+  if (threadIdx.x == 0) report_error(err, LH_ERR_DEVICE, 404);
+  return 0;
+}
 
 constexpr int kDiffTileTC = 128;  // rows per tile of the tensor-core kernels
 constexpr int kDiffTileFP = 64;   // of the fp32 kernels
 
 __host__ __device__ __forceinline__ int diff_ntile(int T, int B, int ts) { return (T + ts - 1) / ts + B; }
+// Sequences of a call at most: placing a tile takes one look at each.
+constexpr int kDiffMaxSeqs = 65536;
 
 // rows [lo, hi) of sequence b, inside [0, T) whatever cu holds
 __device__ __forceinline__ void diff_seq(const DiffGeom& g, int b, int& lo, int& hi) {
@@ -55,11 +67,12 @@ cudaError_t launch_diff_dlam(int H, int n, const float* part, lh_dtype dt, void*
 
 // om: both maps' outputs [T][H][2][D], lse (base 2) [H][2][T]; NULL where no backward follows
 cudaError_t launch_diff_fwd_fp(const DiffGeom& g, lh_dtype dt, const void* q, const void* k, const void* v,
-                               const void* lam, const DiffTile* tiles, void* o, float* om, float* lse, cudaStream_t s);
+                               const void* lam, const DiffTile* tiles, void* o, float* om, float* lse, int* err,
+                               cudaStream_t s);
 cudaError_t launch_diff_bwd_fp(const DiffGeom& g, lh_dtype dt, const void* dout, const void* q, const void* k,
                                const void* v, const void* lam, const DiffTile* tiles, const float* om,
                                const float* lse, float* delta, float* part, void* dq, void* dk, void* dv, void* dlam,
-                               cudaStream_t s);
+                               int* err, cudaStream_t s);
 
 constexpr int kDiffDeltaRows = 64;   // rows per block of the delta kernel (one partial sum of dlam each)
 

@@ -42,7 +42,7 @@ namespace cg = cooperative_groups;
 
 // Blocks per tile: enough for two on every SM, no more than the longest walk has
 // tiles.
-int split_of(int blocks, int T) {
+int split_of(long long blocks, long long T) {
   int s = 1;
   while (s < kMaxSplit && blocks * s < 2 * 148 && 2 * s * TS <= T + TS) s *= 2;
   return s;
@@ -177,12 +177,12 @@ template <typename T, int D>
 __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* __restrict__ q, const T* __restrict__ k,
                                                     const T* __restrict__ v, const void* lam, const DiffTile* tiles,
                                                     T* __restrict__ o, float* __restrict__ om, float* __restrict__ lse,
-                                                    int split) {
+                                                    int split, int* err) {
   constexpr int LD = D + 4, W = D / 16, DM = D / 2;
   extern __shared__ __align__(16) float smf[];
   float *Q = smf, *K = Q + TS * LD, *V = K + TS * LD, *P = V + TS * LD;    // P: two maps
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-  if (tile >= tiles[g.ntile].x) return;           // the whole cluster
+  if (tile >= diff_used(tiles, g, err)) return;           // the whole cluster
   const DiffTile t = tiles[tile];
   const int h = blockIdx.y, hk = h / g.G;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -356,12 +356,12 @@ template <typename T, int D>
 __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __restrict__ dout, const T* __restrict__ q,
                                                    const T* __restrict__ k, const T* __restrict__ v, const void* lam,
                                                    const DiffTile* tiles, const float* __restrict__ lse,
-                                                   const float* __restrict__ delta, T* __restrict__ dq, int split) {
+                                                   const float* __restrict__ delta, T* __restrict__ dq, int split, int* err) {
   constexpr int LD = D + 4, DM = D / 2, W = DM / 16;
   extern __shared__ __align__(16) float smf[];
   float *Q = smf, *O = Q + TS * LD, *K = O + TS * LD, *V = K + TS * LD, *S = V + TS * LD;
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-  if (tile >= tiles[g.ntile].x) return;           // the whole cluster
+  if (tile >= diff_used(tiles, g, err)) return;           // the whole cluster
   const DiffTile t = tiles[tile];
   const int h = blockIdx.y, hk = h / g.G;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -441,12 +441,12 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
                                                      const T* __restrict__ q, const T* __restrict__ k,
                                                      const T* __restrict__ v, const void* lam, const DiffTile* tiles,
                                                      const float* __restrict__ lse, const float* __restrict__ delta,
-                                                     T* __restrict__ dk, T* __restrict__ dv, int split) {
+                                                     T* __restrict__ dk, T* __restrict__ dv, int split, int* err) {
   constexpr int LD = D + 4, DM = D / 2, W = DM / 16, WV = D / 16;
   extern __shared__ __align__(16) float smf[];
   float *K = smf, *V = K + TS * LD, *Q = V + TS * LD, *O = Q + TS * LD, *S = O + TS * LD, *vec = S + TS * LP;
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-  if (tile >= tiles[g.ntile].x) return;
+  if (tile >= diff_used(tiles, g, err)) return;
   const DiffTile t = tiles[tile];
   const int ntl = (t.y + TS - 1) / TS, jt = ntl - 1 - t.w;      // early key tiles first: they have the most queries
   const int hk = blockIdx.y;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
 
 // grid (tiles * split, heads), clusters of `split` blocks along x
 template <typename K, typename... A>
-cudaError_t launch_split(K kern, int ntile, int heads, int split, int sm, cudaStream_t s, A... args) {
+cudaError_t launch_split(K kern, int ntile, int heads, int split, int sm, int* err, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(ntile * split, heads);
   c.blockDim = dim3(NT);
@@ -553,23 +553,23 @@ cudaError_t launch_split(K kern, int ntile, int heads, int split, int sm, cudaSt
   c.attrs = at;
   c.numAttrs = 1;
   count_launch();
-  return cudaLaunchKernelEx(&c, kern, args..., split);
+  return cudaLaunchKernelEx(&c, kern, args..., split, err);
 }
 
 template <typename T, int D>
 cudaError_t fwd_t(const DiffGeom& g, const void* q, const void* k, const void* v, const void* lam, const DiffTile* tiles,
-                  void* o, float* om, float* lse, cudaStream_t s) {
+                  void* o, float* om, float* lse, int* err, cudaStream_t s) {
   const int sm = (3 * TS * (D + 4) + 2 * TS * LP) * 4;
   auto kern = k_diff_fwd_fp<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
   if (e != cudaSuccess) return e;
-  return launch_split(kern, g.ntile, g.H, split_of(g.ntile * g.H, g.T), sm, s, g, (const T*)q, (const T*)k, (const T*)v, lam,
+  return launch_split(kern, g.ntile, g.H, split_of((long long)g.ntile * g.H, g.T), sm, err, s, g, (const T*)q, (const T*)k, (const T*)v, lam,
                       tiles, (T*)o, om, lse);
 }
 
 template <typename T, int D>
 cudaError_t bwd_t(const DiffGeom& g, const void* dout, const void* q, const void* k, const void* v, const void* lam,
-                  const DiffTile* tiles, const float* lse, const float* delta, void* dq, void* dk, void* dv,
+                  const DiffTile* tiles, const float* lse, const float* delta, void* dq, void* dk, void* dv, int* err,
                   cudaStream_t s) {
   const int sm1 = (4 * TS * (D + 4) + 2 * TS * LP) * 4, sm2 = (4 * TS * (D + 4) + TS * LP + 256) * 4;
   auto kq = k_diff_dq_fp<T, D>;
@@ -578,28 +578,29 @@ cudaError_t bwd_t(const DiffGeom& g, const void* dout, const void* q, const void
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, sm2);
   if (e != cudaSuccess) return e;
-  e = launch_split(kk, g.ntile, g.Hk, split_of(g.ntile * g.Hk, g.T * g.G), sm2, s, g, (const T*)dout, (const T*)q,
+  e = launch_split(kk, g.ntile, g.Hk, split_of((long long)g.ntile * g.Hk, (long long)g.T * g.G), sm2, err, s, g, (const T*)dout, (const T*)q,
                    (const T*)k, (const T*)v, lam, tiles, lse, delta, (T*)dk, (T*)dv);
   if (e != cudaSuccess) return e;
-  return launch_split(kq, g.ntile, g.H, split_of(g.ntile * g.H, g.T), sm1, s, g, (const T*)dout, (const T*)q, (const T*)k,
+  return launch_split(kq, g.ntile, g.H, split_of((long long)g.ntile * g.H, g.T), sm1, err, s, g, (const T*)dout, (const T*)q, (const T*)k,
                       (const T*)v, lam, tiles, lse, delta, (T*)dq);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_fwd_fp(const DiffGeom& g, lh_dtype dt, const void* q, const void* k, const void* v,
-                               const void* lam, const DiffTile* tiles, void* o, float* om, float* lse, cudaStream_t s) {
+                               const void* lam, const DiffTile* tiles, void* o, float* om, float* lse, int* err,
+                               cudaStream_t s) {
   if (dt == LH_BF16)
-    return g.D == 64 ? fwd_t<__nv_bfloat16, 64>(g, q, k, v, lam, tiles, o, om, lse, s)
-                     : fwd_t<__nv_bfloat16, 128>(g, q, k, v, lam, tiles, o, om, lse, s);
-  return g.D == 64 ? fwd_t<float, 64>(g, q, k, v, lam, tiles, o, om, lse, s)
-                   : fwd_t<float, 128>(g, q, k, v, lam, tiles, o, om, lse, s);
+    return g.D == 64 ? fwd_t<__nv_bfloat16, 64>(g, q, k, v, lam, tiles, o, om, lse, err, s)
+                     : fwd_t<__nv_bfloat16, 128>(g, q, k, v, lam, tiles, o, om, lse, err, s);
+  return g.D == 64 ? fwd_t<float, 64>(g, q, k, v, lam, tiles, o, om, lse, err, s)
+                   : fwd_t<float, 128>(g, q, k, v, lam, tiles, o, om, lse, err, s);
 }
 
 cudaError_t launch_diff_bwd_fp(const DiffGeom& g, lh_dtype dt, const void* dout, const void* q, const void* k,
                                const void* v, const void* lam, const DiffTile* tiles, const float* om,
                                const float* lse, float* delta, float* part, void* dq, void* dk, void* dv, void* dlam,
-                               cudaStream_t s) {
+                               int* err, cudaStream_t s) {
   const int nb = (g.T + kDiffDeltaRows - 1) / kDiffDeltaRows;
   const dim3 gd(nb, g.H);
   if (dt == LH_BF16)
@@ -611,10 +612,10 @@ cudaError_t launch_diff_bwd_fp(const DiffGeom& g, lh_dtype dt, const void* dout,
   if (e != cudaSuccess) return e;
   if ((e = launch_diff_dlam(g.H, nb, part, dt, dlam, s)) != cudaSuccess) return e;
   if (dt == LH_BF16)
-    return g.D == 64 ? bwd_t<__nv_bfloat16, 64>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, s)
-                     : bwd_t<__nv_bfloat16, 128>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, s);
-  return g.D == 64 ? bwd_t<float, 64>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, s)
-                   : bwd_t<float, 128>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, s);
+    return g.D == 64 ? bwd_t<__nv_bfloat16, 64>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, err, s)
+                     : bwd_t<__nv_bfloat16, 128>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, err, s);
+  return g.D == 64 ? bwd_t<float, 64>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, err, s)
+                   : bwd_t<float, 128>(g, dout, q, k, v, lam, tiles, lse, delta, dq, dk, dv, err, s);
 }
 
 }  // namespace lh

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_
                                                    const __nv_bfloat16* v, __half* qs, __half* ks, __half* vs,
                                                    const DiffTile* tiles, const int* seq, uint32_t* amax, int* err) {
   pdl_start();
-  if ((int)blockIdx.x >= tiles[g.ntile].x) return;
+  if ((int)blockIdx.x >= diff_used(tiles, g, err)) return;
   const int y = blockIdx.y;
   const int which = y < g.H ? kScaleQ : y < g.H + g.Hk ? kScaleK : kScaleV;
   const int hd = which == kScaleQ ? y : which == kScaleK ? y - g.H : y - g.H - g.Hk;
@@ -144,7 +144,7 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   // long tiles of all heads first
   const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
   pdl_start();
-  if (rank >= tiles[g.ntile].x) return;                          // whole CTA, before any set-up
+  if (rank >= diff_used(tiles, g, err)) return;              // whole CTA, before any set-up
   const DiffTile t = tiles[rank];
   const int nkv = t.w + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -329,7 +329,7 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   uint8_t* sm = smem_raw + Lay::HEAD;
   const int rank = (int)blockIdx.x % g.ntile, hk = (int)blockIdx.x / g.ntile;
   pdl_start();
-  if (rank >= tiles[g.ntile].x) return;
+  if (rank >= diff_used(tiles, g, err)) return;
   if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
   const DiffTile tl = tiles[rank];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -602,7 +602,7 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
   float* red = reinterpret_cast<float*>(smem_raw + 256);          // the compute warps' sums of A2 dP
   const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
   pdl_start();
-  if (rank >= tiles[g.ntile].x) {
+  if (rank >= diff_used(tiles, g, err)) {
     if (threadIdx.x == 0) part[(size_t)h * g.ntile + rank] = 0.f;
     return;
   }
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __
   constexpr int L = D / 8, RPB = 256 / L;      // lanes per row, rows per step
   const int h = blockIdx.y, hk = h / g.G, lane = threadIdx.x & 31;
   if (REDO) pdl_start();
-  if ((int)blockIdx.x >= tiles[g.ntile].x) return;
+  if ((int)blockIdx.x >= diff_used(tiles, g, err)) return;
   const DiffTile t = tiles[blockIdx.x];
   const size_t sh = (size_t)seq[blockIdx.x] * g.Hk + hk;
   float mul = 1.f;

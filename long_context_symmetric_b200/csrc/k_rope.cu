@@ -169,7 +169,7 @@ cudaError_t rope_t(RopeArgs a, int tail, cudaStream_t st) {
   const int items = a.rows * a.per_row;
   // groups of tokens that a block of th threads takes
   auto lanes_of = [&](int th) {
-    const int fit = kRopeSmem / (kTok * a.R * (int)sizeof(float2)), groups = (a.N + kTok - 1) / kTok;
+    const int fit = kRopeSmem / (kTok * a.R * (int)sizeof(float2)), groups = (int)((a.N + kTok - 1LL) / kTok);
     int l = th / items;
     l = l < fit ? l : fit;
     l = l < groups ? l : groups;
@@ -184,13 +184,13 @@ cudaError_t rope_t(RopeArgs a, int tail, cudaStream_t st) {
     const int n = items * lanes_of(th);
     return (double)n / ((double)((n + th - 1) / th) * th);
   };
-  const bool few = (long long)a.B * ((a.N + kTok - 1) / kTok) < 148 * 4;
+  const bool few = a.B * ((a.N + kTok - 1LL) / kTok) < 148 * 4;
   const int th = few || busy(256) > 1.1 * busy(64) ? 256 : 64;
   a.lanes = lanes_of(th);
   a.m_row = ((1ull << 36) + a.per_row - 1) / a.per_row;
   a.m_tok = ((1ull << 36) + items - 1) / items;
   const int toks = a.lanes * kTok;
-  const dim3 grid((a.N + toks - 1) / toks, a.B < 65535 ? a.B : 65535, (a.B + 65534) / 65535);
+  const dim3 grid((unsigned)((a.N + toks - 1LL) / toks), a.B < 65535 ? a.B : 65535, (a.B + 65534) / 65535);
   // moved bytes beyond twice L2 (126 MB): 1.41 -> 1.34 ms at 512K tokens of 32
   // heads of 128; below that what was rotated may still be read from L2
   const bool stream = 2.0 * a.B * a.N * a.rows * a.D * sizeof(T) > 2.5e8;

@@ -561,6 +561,10 @@ lh_status check_norm(const lh_norm_config* c) {
   if (!(c->eps >= 0.f) || std::isinf(c->eps)) return LH_ERR_SHAPE;
   return LH_OK;
 }
+// rows that are written where others of another stride are still to be read
+bool in_place_ok(const lh_norm_config& c, const void* x, const void* y) {
+  return x != y || c.M < 2 || (c.ldx ? c.ldx : c.d) == (c.ldy ? c.ldy : c.d);
+}
 #define LH_OPT(p) do { if (!aligned16(p)) return LH_ERR_ALIGN; } while (0)
 // per-row or per-token values, read and written one by one: their own size
 #define LH_ELEM(p, size) do { if ((uintptr_t)(p) & ((size) - 1)) return LH_ERR_ALIGN; } while (0)
@@ -580,6 +584,7 @@ lh_status lh_norm_fwd(const lh_norm_config* cfg, const void* x, const void* w, c
   if (st != LH_OK) return st;
   if (cfg->M == 0) return LH_OK;
   LH_REQ(x); LH_REQ(y); LH_OPT(w); LH_OPT(b); LH_ELEM(mean, 4); LH_ELEM(rstd, 4);
+  if (!in_place_ok(*cfg, x, y)) return LH_ERR_SHAPE;
   LH_CUDA(launch_norm_fwd(*cfg, x, w, b, y, mean, rstd, (cudaStream_t)stream));
   return LH_OK;
 }
@@ -592,6 +597,7 @@ lh_status lh_norm_bwd(const lh_norm_config* cfg, const void* dy, const void* x, 
   LH_OPT(w); LH_OPT(dw); LH_OPT(db);
   if (cfg->M > 0) {
     LH_REQ(dy); LH_REQ(x); LH_REQ(dx);
+    if (!in_place_ok(*cfg, dx, dy)) return LH_ERR_SHAPE;
     if (!mean || !rstd) return LH_ERR_NULL;
     LH_ELEM(mean, 4); LH_ELEM(rstd, 4);
     if (dw || db) {
@@ -627,6 +633,13 @@ lh_status lh_rope(const lh_rope_config* c, const void* q, const void* k, const v
   if (!pos) return LH_ERR_NULL;
   LH_ELEM(pos, c->pos64 ? 8 : 4);
   if (c->Hk) { LH_REQ(k); LH_REQ(ko); }
+  // in place: the same strides on both sides
+  auto moved = [c](const void* in, const void* out, long long w, long long li, long long lo, long long bi, long long bo) {
+    li = li ? li : w; lo = lo ? lo : w;
+    return in == out && ((c->N > 1 && li != lo) || (c->B > 1 && (bi ? bi : li * c->N) != (bo ? bo : lo * c->N)));
+  };
+  if (moved(q, qo, wq, c->q_ld, c->qo_ld, c->q_bs, c->qo_bs)) return LH_ERR_SHAPE;
+  if (c->Hk && moved(k, ko, wk, c->k_ld, c->ko_ld, c->k_bs, c->ko_bs)) return LH_ERR_SHAPE;
   int* err = device_error_ptr();
   if (!err) return LH_ERR_CUDA;
   LH_CUDA(launch_rope(*c, q, k, pos, freq, axis, inverse, qo, ko, err, (cudaStream_t)stream));
@@ -650,7 +663,7 @@ lh_status make_diff(const lh_diff_config* c, DiffGeom* g, DiffSizes* z) {
   if (!c) return LH_ERR_NULL;
   if (c->dtype != LH_BF16 && c->dtype != LH_FP32) return LH_ERR_DTYPE;
   if ((unsigned)c->packed > 1u || (unsigned)c->train > 1u) return LH_ERR_MODE;
-  if (c->B < 1 || c->B > (1 << 20) || c->T < 0 || c->T >= (1 << 30)) return LH_ERR_SHAPE;
+  if (c->B < 1 || c->B > kDiffMaxSeqs || c->T < 0 || c->T >= (1 << 30)) return LH_ERR_SHAPE;
   if (c->H < 1 || c->H > (1 << 15) || c->Hk < 1 || c->H % c->Hk || (c->D != 64 && c->D != 128)) return LH_ERR_SHAPE;
   if (!c->packed && c->T % c->B) return LH_ERR_SHAPE;
   const long long wq = (long long)c->H * c->D, wk = (long long)c->Hk * c->D;
@@ -669,6 +682,12 @@ lh_status make_diff(const lh_diff_config* c, DiffGeom* g, DiffSizes* z) {
   const size_t T = c->T, H = c->H, D = c->D;
   z->tc = c->dtype == LH_BF16 && !force_simt();
   g->ntile = diff_ntile(c->T, c->B, z->tc ? kDiffTileTC : kDiffTileFP);
+  // grid limits
+  if ((long long)g->ntile * c->H > 0x7fffffffLL || c->H + 2 * c->Hk > 65535) return LH_ERR_SHAPE;
+  // what the saved buffer depends on, mixed into a word (FNV-1a)
+  uint32_t tag = 2166136261u;
+  for (int v : {c->B, c->T, c->H, c->Hk, c->D, (int)c->dtype, c->packed, c->train, z->tc}) tag = (tag ^ (uint32_t)v) * 16777619u;
+  g->tag = (int)tag;
   const size_t R = z->tc ? (size_t)g->ntile * kDiffTileTC : T, Hk = c->Hk;     // rows of the statistics
   size_t at = 0;
   auto part = [&at](size_t bytes) { const size_t p = at; at += up256(bytes); return p; };
@@ -756,7 +775,7 @@ lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void*
     return LH_OK;
   }
   LH_CUDA(launch_diff_tiles(g, kDiffTileFP, tiles, nullptr, nullptr, err, s));
-  LH_CUDA(launch_diff_fwd_fp(g, cfg->dtype, q, k, v, lam, tiles, o, om, lse, s));
+  LH_CUDA(launch_diff_fwd_fp(g, cfg->dtype, q, k, v, lam, tiles, o, om, lse, err, s));
   return LH_OK;
 }
 
@@ -791,7 +810,7 @@ lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const vo
   LH_CUDA(launch_diff_bwd_fp(g, cfg->dtype, dout, q, k, v, lam, reinterpret_cast<const DiffTile*>(sv + z.tiles),
                              reinterpret_cast<const float*>(sv + z.om), reinterpret_cast<const float*>(sv + z.lse),
                              reinterpret_cast<float*>(w + z.delta), reinterpret_cast<float*>(w + z.part), dq, dk, dv,
-                             dlam, s));
+                             dlam, err, s));
   return LH_OK;
 }
 

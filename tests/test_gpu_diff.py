@@ -1,5 +1,7 @@
 """Causal differential attention, forward and backward, against its 64-bit form."""
 
+import os
+
 import pytest
 import torch
 
@@ -256,3 +258,61 @@ def test_dlam_of_a_sum_that_cancels(dtype):
     rel = (2 * 68 * 16 + 136 + 64 + 2 ** 3) * U + 2.0 ** -21
     tol = 8 * rel * float(mag.square().sum().sqrt()) + (N / 2 + 64) * U * float(terms.abs().sum()) / N ** 0.5
     assert abs(float(got - want)) <= tol + HALF[dtype] * abs(float(want)), (float(got), float(want), tol)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_saved_buffer_of_another_problem_is_not_followed(dtype):
+    q, k, v, lam, do = inputs(121, 300, 2, 1, 64, dtype)
+    cfg = lh.make_diff_config(1, 300, 2, 64, dtype, 1)
+    other = lh.make_diff_config(2, 150, 2, 64, dtype, 1)      # the same rows, cut otherwise
+    ws, o = lh.DiffWorkspace(other, DEV), torch.empty_like(q)   # as large as either needs
+    grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    dlam = torch.empty_like(lam)
+    ws.saved.fill_(255)                               # never written
+    lh.diff_attn_bwd(cfg, do, q, k, v, lam, ws, *grads, dlam)
+    assert lh.get_device_error() == (9, 404)
+    lh.diff_attn_fwd(other, q, k, v, lam, o, ws)
+    lh.diff_attn_bwd(cfg, do, q, k, v, lam, ws, *grads, dlam)
+    assert lh.get_device_error() == (9, 404)
+    assert all((t == 7).all() for t in grads)
+
+
+def test_non_finite_values_are_reported_and_stay_in_their_head():
+    q, k, v, lam, do = inputs(131, 200, 4, 2, 128, "bf16")
+    cfg = lh.make_diff_config(1, 200, 4, 128, "bf16", 2)
+    ref = run(cfg, q, k, v, lam, do)
+    v2 = v.clone()
+    v2[77, 1, 5] = float("nan")
+    ws, o = lh.DiffWorkspace(cfg, DEV), torch.empty_like(q)
+    lh.diff_attn_fwd(cfg, q, k, v2, lam, o, ws)
+    assert lh.get_device_error() == ((0, 0) if os.environ.get("LH_ATTN_SIMT", "").startswith("1") else (9, 102))
+    assert torch.equal(o[:, :2], ref["o"][:, :2]) and o[77:, 2:].isnan().any(-1).all()
+    assert torch.equal(run(cfg, q, k, v, lam, do)["dk"], ref["dk"])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_short_sequences(dtype):
+    """1,500 sequences of 0 to 3 tokens."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 4, (1500,), generator=g)
+    ends = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    T = int(ends[-1])
+    q, k, v, lam, do = inputs(141, T, 1, 1, 64, dtype)
+    cfg = lh.make_diff_config(1500, 0, 1, 64, dtype, rows=T)
+    got = run(cfg, q, k, v, lam, do, cu=ends.to(torch.int32).to(DEV))
+    check(got, q, k, v, lam, do, list(zip(ends.tolist(), ends[1:].tolist())), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_offsets_past_32_bits(dtype):
+    """Token rows 2^24 elements apart: the last ones start beyond element 2^31."""
+    N, D, ld = 140, 64, 1 << 24
+    q, k, v, lam, do = inputs(151, N, 1, 1, D, dtype)
+    far = torch.empty((N - 1) * ld + D, dtype=DT[dtype], device=DEV).as_strided((N, D), (ld, 1))
+    far.copy_(k[:, 0])
+    want = run(lh.make_diff_config(1, N, 1, D, dtype), q, k, v, lam, do)["o"]
+    cfg = lh.make_diff_config(1, N, 1, D, dtype, ldk=ld)
+    o = torch.empty_like(q)
+    lh.diff_attn_fwd(cfg, q, far, v, lam, o, lh.DiffWorkspace(cfg, DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)

@@ -172,3 +172,16 @@ def test_another_stream():
     with torch.cuda.stream(st):
         got = run(x, w, w, dy, "bf16", "bf16")
     assert all(torch.equal(got[n], ref[n]) for n in ref)
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^25 elements apart: the last ones start beyond element 2^31."""
+    M, d, ld = 70, 320, 1 << 25
+    x, w = rand(1, M, d, dtype="bf16"), rand(3, d, dtype="bf16")
+    far = torch.empty((M - 1) * ld + d, dtype=torch.bfloat16, device=DEV).as_strided((M, d), (ld, 1))
+    far.copy_(x)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    lh.norm_fwd(lh.make_norm_config(M, d), x, w, None, a)
+    lh.norm_fwd(lh.make_norm_config(M, d, ldx=ld), far, w, None, b)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)

@@ -163,3 +163,17 @@ def test_graph_and_another_stream():
     lh.rope(cfg, q, k, pos, plan.freq, plan.axis, q2, k2, stream=st)
     torch.cuda.synchronize()
     assert torch.equal(qo, rq) and torch.equal(ko, rk) and torch.equal(q2, rq) and torch.equal(k2, rk)
+
+
+def test_offsets_past_32_bits():
+    """Token rows 2^25 elements apart, in place: the last ones start beyond element 2^31."""
+    N, D, ld = 70, 64, 1 << 25
+    q = rand(1, 1, N, 1, D, dtype="bf16")
+    plan, pos = lh.RopePlan(D, device=DEV), positions(3, 1, 1, N)
+    want = torch.empty_like(q)
+    lh.rope(lh.make_rope_config(1, N, 1, 0, D), q, None, pos, plan.freq, plan.axis, want, None)
+    far = torch.empty((N - 1) * ld + D, dtype=torch.bfloat16, device=DEV).as_strided((N, D), (ld, 1))
+    far.copy_(q[0, :, 0])
+    lh.rope(lh.make_rope_config(1, N, 1, 0, D, q_ld=ld, qo_ld=ld), far, None, pos, plan.freq, plan.axis, far, None)
+    torch.cuda.synchronize()
+    assert torch.equal(far, want[0, :, 0])

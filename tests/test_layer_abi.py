@@ -201,3 +201,19 @@ def test_rope_plan_tables():
     own = [10000.0 ** (-i / 4) for i in range(4)], [10000.0 ** (-i / 2) for i in range(2)]
     assert torch.allclose(p.freq, torch.tensor([own[0][0], own[1][0], own[1][0], own[0][1], own[1][1], own[1][1], own[0][2], own[0][3]],
                                                dtype=torch.float64), rtol=1e-15)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=65537, T=65537), dict(T=1 << 29, H=1 << 12), dict(H=1 << 15, Hk=1 << 14)])
+def test_diff_refuses_what_no_grid_holds(kw):
+    test_diff_refuses(kw, SHAPE)
+
+
+def test_in_place_needs_equal_strides():
+    f, before = lh.lib(), lh.launch_count()
+    c = ctypes.byref(lh.make_norm_config(4, 64, ldx=128))
+    assert f.lh_norm_fwd(c, A, A, None, A, None, None, None) == SHAPE
+    assert f.lh_norm_bwd(c, A, A + 4096, None, A, A, A, None, None, None, 0, None) == SHAPE
+    for kw in (dict(q_ld=512), dict(ko_ld=512), dict(q_bs=1 << 16), dict(ko_bs=1 << 16)):
+        assert f.lh_rope(ctypes.byref(rope(**kw)), A, A + 4096, A, A, A, 0, A, A + 4096, None) == SHAPE
+    assert lh.launch_count() == before
