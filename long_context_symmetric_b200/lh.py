@@ -455,13 +455,45 @@ def _need(name, dev, label, t, dt, n):
     raise ValueError(f"{name}: {label} of shape {tuple(t.shape)}: {n} contiguous elements are wanted")
 
 
-def _rows_fit(name, dev, label, t, dt, rows, ld, width):
-    """rows x width elements, ld apart, lie in the tensor's storage."""
-    n = (rows - 1) * ld + width if rows else 0
+def _walks_as(t, width, rows, ld, per, bs):
+    """A tensor that is not contiguous steps as the call will: dense rows of `width` elements, ld apart, each `per`
+    of them bs apart. (A dense stretch longer than a row is taken as a buffer that the call's strides cut up.)"""
+    want, nxt, seen = 1, None, 1
+    steps = ([ld] if per > 1 else []) + ([bs] if rows > per else [])
+    for size, stride in zip(reversed(t.shape), reversed(t.stride())):
+        if size == 1:
+            continue
+        if want < width:
+            if stride != want:
+                return False
+            want *= size
+        elif want > width or seen >= rows:
+            return True
+        else:
+            # the next level, or this one's continuation in a tensor of more axes
+            if steps and stride == steps[0]:
+                steps.pop(0)
+            elif stride != nxt:
+                return False
+            nxt = stride * size
+            seen *= size
+    return True
+
+
+def _rows_fit(name, dev, label, t, dt, rows, ld, width, per=0, bs=0):
+    """rows x width elements, ld apart (each `per` of them bs apart), lie in the tensor's storage, and its strides are
+    the call's."""
+    if not per:
+        n = (rows - 1) * ld + width if rows else 0
+    else:
+        n = (rows // per - 1) * bs + (per - 1) * ld + width
     if t.dtype is dt and t.device == dev:
         # a contiguous tensor of that size, or room enough behind a view's first element
-        if t.numel() >= n and t.is_contiguous():
-            return
+        if t.is_contiguous():
+            if t.numel() >= n:
+                return
+        elif not _walks_as(t, width, rows, ld, per or rows, bs):
+            raise ValueError(f"{name}: {label} has strides {tuple(t.stride())}, the call's rows of {width} are {ld} apart")
         if n <= t.untyped_storage().nbytes() // t.element_size() - t.storage_offset():
             return
     _refuse(name, dev, label, t, dt)
@@ -539,9 +571,12 @@ def rope(cfg, q, k, pos, freq, axis, qo, ko, inverse=False, stream=None):
                                         ("k", k, cfg.Hk, cfg.k_ld, cfg.k_bs), ("ko", ko, cfg.Hk, cfg.ko_ld, cfg.ko_bs)):
             if heads:
                 ld = ld or heads * D
-                _rows_fit(f, dev, label, t, dt, 1, 0, (B - 1) * (bs or N * ld) + (N - 1) * ld + heads * D)
-        _rows_fit(f, dev, "pos", pos, torch.int64 if cfg.pos64 else torch.int32, 1, 0,
-                  (cfg.axes - 1) * cfg.pos_as + (B - 1) * cfg.pos_bs + N)
+                _rows_fit(f, dev, label, t, dt, B * N, ld, heads * D, N, bs or N * ld)
+        # rows of N positions, pos_bs apart, in axes * B (shared: axes) of them
+        if cfg.pos_bs:
+            _rows_fit(f, dev, "pos", pos, torch.int64 if cfg.pos64 else torch.int32, cfg.axes * B, cfg.pos_bs, N, B, cfg.pos_as)
+        else:
+            _rows_fit(f, dev, "pos", pos, torch.int64 if cfg.pos64 else torch.int32, cfg.axes, cfg.pos_as, N)
     _need(f, dev, "freq", freq, torch.float64, R)
     _need(f, dev, "axis", axis, torch.int32, R)
     _call(f, dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(pos), _p(freq), _p(axis), int(inverse), _p(qo), _p(ko))
@@ -734,7 +769,7 @@ def rotary(q, k, pos, plan: RopePlan, pairs: str = "half"):
 
 class DifferentialAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, lam, cu):
+    def forward(ctx, q, k, v, lam, cu, train=True):
         packed = cu is not None
         if q.ndim != (3 if packed else 4) or k.shape != v.shape or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
             raise ValueError(f"differential_attention: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not "
@@ -745,8 +780,8 @@ class DifferentialAttention(torch.autograd.Function):
             raise ValueError("differential_attention: k, v and lam [H] have q's type")
         q, k, v, lam = (_whole(t) for t in (q, k, v, lam))
         name = type_name(q, "differential_attention")
-        cfg = (make_diff_config(cu.numel() - 1, 0, H, D, name, Hk, rows=q.shape[0]) if packed
-               else make_diff_config(q.shape[0], q.shape[1], H, D, name, Hk))
+        cfg = (make_diff_config(cu.numel() - 1, 0, H, D, name, Hk, rows=q.shape[0], train=train) if packed
+               else make_diff_config(q.shape[0], q.shape[1], H, D, name, Hk, train=train))
         ws = DiffWorkspace(cfg, q.device)
         # packed: rows outside the sequences are not written by the kernels
         o = torch.zeros_like(q) if packed else torch.empty_like(q)
@@ -762,10 +797,12 @@ class DifferentialAttention(torch.autograd.Function):
         new = torch.zeros_like if ctx.cfg.packed else torch.empty_like
         dq, dk, dv, dlam = new(q), new(k), new(v), torch.empty_like(lam)
         diff_attn_bwd(ctx.cfg, _whole(do), q, k, v, lam, ctx.ws, dq, dk, dv, dlam, cu=cu)
-        return dq, dk, dv, dlam, None
+        return dq, dk, dv, dlam, None, None
 
 
 def differential_attention(q, k, v, lam, cu=None):
     """o = (softmax map 1 - lam * softmax map 2) v, causal; q [B, N, H, D], k, v [B, N, Hk, D], lam [H]. With cu
     (int32 [sequences + 1], device): q [T, H, D] and so on, the sequences packed one behind the other."""
-    return DifferentialAttention.apply(q, k, v, lam, cu)
+    # without a backward pass to come nothing is kept for one
+    train = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
+    return DifferentialAttention.apply(q, k, v, lam, cu, train)

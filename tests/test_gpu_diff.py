@@ -316,3 +316,18 @@ def test_offsets_past_32_bits(dtype):
     lh.diff_attn_fwd(cfg, q, far, v, lam, o, lh.DiffWorkspace(cfg, DEV))
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_without_gradients_nothing_is_kept_for_them(dtype, monkeypatch):
+    q, k, v, lam, do = inputs(161, 130, 2, 1, 64, dtype)
+    q, k, v = (t[None] for t in (q, k, v))
+    made, make = [], lh.make_diff_config
+    monkeypatch.setattr(lh, "make_diff_config", lambda *a, **kw: made.append(make(*a, **kw)) or made[-1])
+    a = lh.differential_attention(q, k, v, lam)
+    with torch.no_grad():
+        b = lh.differential_attention(q.clone().requires_grad_(), k, v, lam)
+    c = lh.differential_attention(q, k, v, lam.clone().requires_grad_())
+    c.backward(do[None])
+    assert [m.train for m in made] == [0, 0, 1]
+    assert torch.equal(a, b) and torch.equal(a, c.detach()) and lh.get_device_error() == (0, 0)

@@ -4,6 +4,7 @@ CUDA call, and the binding refuses tensors that do not fit a call."""
 
 import ctypes
 import math
+import types
 
 import pytest
 import torch
@@ -217,3 +218,34 @@ def test_in_place_needs_equal_strides():
     for kw in (dict(q_ld=512), dict(ko_ld=512), dict(q_bs=1 << 16), dict(ko_bs=1 << 16)):
         assert f.lh_rope(ctypes.byref(rope(**kw)), A, A + 4096, A, A, A, 0, A, A + 4096, None) == SHAPE
     assert lh.launch_count() == before
+
+
+def test_binding_refuses_strides_that_are_not_the_calls():
+    """A view that steps otherwise than the configuration says is refused; one that steps so reaches the library
+    (which refuses these calls for other reasons, before any CUDA call)."""
+    bf, legacy = torch.bfloat16, types.SimpleNamespace(cuda_stream=None)
+    wide = torch.zeros(4, 9, 80, dtype=bf)[:, :5, :64]
+    y = torch.empty(20, 64, dtype=bf)
+    for x, kw in ((wide, {}), (wide, dict(ldx=80)), (torch.zeros(64, 20, dtype=bf).t(), {}),
+                  (torch.zeros(64, dtype=bf).expand(20, 64), {})):
+        with pytest.raises(ValueError, match="x has strides"):
+            lh.norm_fwd(lh.make_norm_config(20, 64, **kw), x, None, None, y)
+    with pytest.raises(lh.LHError, match="status 2"):
+        lh.norm_fwd(lh.make_norm_config(20, 64, eps=-1.0, ldx=80), torch.zeros(4, 5, 80, dtype=bf)[..., :64], None, None, y,
+                    stream=legacy)
+    plan, pos = lh.RopePlan(64, device="cpu"), torch.zeros(1, 2, 8, dtype=torch.int32)
+    q, k = torch.zeros(2, 8, 2, 64, dtype=bf), torch.zeros(2, 8, 1, 64, dtype=bf)
+    heads_first = torch.zeros(2, 2, 8, 64, dtype=bf).transpose(1, 2)
+    for bad in (heads_first, torch.zeros(2, 16, 2, 64, dtype=bf)[:, ::2], torch.zeros(2, 9, 2, 64, dtype=bf)[:, :8]):
+        with pytest.raises(ValueError, match="q has strides"):
+            lh.rope(lh.make_rope_config(2, 8, 2, 1, 64), bad, k, pos, plan.freq, plan.axis, q, k)
+    with pytest.raises(ValueError, match="pos has strides"):
+        lh.rope(lh.make_rope_config(2, 8, 2, 1, 64), q, k, torch.zeros(8, 2, dtype=torch.int32).t(), plan.freq, plan.axis, q, k)
+    part = torch.zeros(2, 9, 2, 64, dtype=bf)[:, :8]
+    rc = lh.make_rope_config(2, 8, 2, 1, 64, q_bs=9 * 128)
+    rc.pairs = 5
+    with pytest.raises(lh.LHError, match="status 5"):
+        lh.rope(rc, part, k, pos, plan.freq, plan.axis, q, k, stream=legacy)
+    dc = lh.make_diff_config(2, 8, 2, 64)
+    with pytest.raises(ValueError, match="k has strides"):
+        lh.diff_attn_fwd(dc, q, heads_first, q, q[0, 0, :, 0].contiguous(), q, lh.DiffWorkspace(dc, "cpu"))
