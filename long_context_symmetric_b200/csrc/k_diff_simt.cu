@@ -181,10 +181,12 @@ __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* _
   constexpr int LD = D + 4, W = D / 16, DM = D / 2;
   extern __shared__ __align__(16) float smf[];
   float *Q = smf, *K = Q + TS * LD, *V = K + TS * LD, *P = V + TS * LD;    // P: two maps
-  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int rank = blockIdx.x % split;
+  int tile, h;
+  diff_place(g.oq, blockIdx.x / split, tile, h);
   if (tile >= diff_used(tiles, g, err)) return;           // the whole cluster
   const DiffTile t = tiles[tile];
-  const int h = blockIdx.y, hk = h / g.G;
+  const int hk = h / g.G;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = t.w * TS;                                // first row within the sequence
   const T* kb = k + (long long)t.x * g.ldk + (long long)hk * D;
@@ -360,10 +362,12 @@ __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __
   constexpr int LD = D + 4, DM = D / 2, W = DM / 16;
   extern __shared__ __align__(16) float smf[];
   float *Q = smf, *O = Q + TS * LD, *K = O + TS * LD, *V = K + TS * LD, *S = V + TS * LD;
-  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int rank = blockIdx.x % split;
+  int tile, h;
+  diff_place(g.oq, blockIdx.x / split, tile, h);
   if (tile >= diff_used(tiles, g, err)) return;           // the whole cluster
   const DiffTile t = tiles[tile];
-  const int h = blockIdx.y, hk = h / g.G;
+  const int hk = h / g.G;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = t.w * TS;
   const T* kb = k + (long long)t.x * g.ldk + (long long)hk * D;
@@ -445,11 +449,12 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
   constexpr int LD = D + 4, DM = D / 2, W = DM / 16, WV = D / 16;
   extern __shared__ __align__(16) float smf[];
   float *K = smf, *V = K + TS * LD, *Q = V + TS * LD, *O = Q + TS * LD, *S = O + TS * LD, *vec = S + TS * LP;
-  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-  if (tile >= diff_used(tiles, g, err)) return;
+  const int rank = blockIdx.x % split;
+  int tile, hk;
+  diff_place(g.ok, blockIdx.x / split, tile, hk);
+  if (tile >= diff_used(tiles, g, err)) return;           // the whole cluster
   const DiffTile t = tiles[tile];
   const int ntl = (t.y + TS - 1) / TS, jt = ntl - 1 - t.w;      // early key tiles first: they have the most queries
-  const int hk = blockIdx.y;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int k0 = jt * TS;
   const float sc = rsqrtf((float)DM), c2 = kLog2e * sc;
@@ -538,11 +543,11 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
   }
 }
 
-// grid (tiles * split, heads), clusters of `split` blocks along x
+// a cluster of `split` blocks per tile and head
 template <typename K, typename... A>
 cudaError_t launch_split(K kern, int ntile, int heads, int split, int sm, int* err, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(ntile * split, heads);
+  c.gridDim = dim3((unsigned)ntile * heads * split);
   c.blockDim = dim3(NT);
   c.dynamicSmemBytes = sm;
   c.stream = s;

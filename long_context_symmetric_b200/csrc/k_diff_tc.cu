@@ -141,18 +141,18 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   float* linv = reinterpret_cast<float*>(smem_raw + 256);        // [2][128]
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + Lay::HEAD + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(sm);
-  // long tiles of all heads first
-  const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
-  pdl_start();
-  if (rank >= diff_used(tiles, g, err)) return;              // whole CTA, before any set-up
-  const DiffTile t = tiles[rank];
-  const int nkv = t.w + 1;
+  int rank, h;
+  diff_place(g.oq, blockIdx.x, rank, h);
+  const int hk = h / g.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t* am = amax + (size_t)seq[rank] * g.Hk + hk;
-  const size_t plane = (size_t)g.B * g.Hk;
-  const int ev = diff_exp(am[kScaleV * plane]);
-  c2 *= pow2f(diff_exp(am[kScaleQ * plane]) + diff_exp(am[kScaleK * plane]));
-
+  if (threadIdx.x == 0) {
+    prefetch_map(&tq);
+    prefetch_map(&tk);
+    prefetch_map(&tv);
+  }
+  pdl_start();
+  TileLoad tl;
+  tl.ask(tiles, seq, g, rank);
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     for (int s = 0; s < NST; ++s) {
@@ -181,6 +181,12 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
   volatile Abort* ab = &bars->abort;
+  if (!tl.live(g, rank, err)) {                                  // the whole CTA
+    if (warp == 1) tmem_dealloc(tbase, 512);
+    return;
+  }
+  const DiffTile t = tl.t;
+  const int nkv = t.w + 1;
 
   if (warp < 4) regs_give();
   if (warp == 0) {
@@ -288,6 +294,10 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     const uint32_t la = (uint32_t)(quarter * 32) << 16;
     const uint32_t cS = tbase + la + 256 * m, cO = cS + 128;
     const int row = t.w * 128 + r;                       // within the sequence
+    const uint32_t* am = amax + (size_t)tl.b * g.Hk + hk;
+    const size_t plane = (size_t)g.B * g.Hk;
+    const int ev = diff_exp(am[kScaleV * plane]);
+    c2 *= pow2f(diff_exp(am[kScaleQ * plane]) + diff_exp(am[kScaleK * plane]));
     float m_run = 0.f, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < nkv; ++j) {
@@ -375,11 +385,11 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
       const float i0 = linv[r], i1 = linv[128 + r];
       const float lm = __bfloat162float(lam[h]), pv = pow2f(ev);
       const bool in = row < t.y;
-      __nv_bfloat16* dst = o + (long long)(t.x + row) * g.ldo + (long long)h * D;
       const size_t prow = (size_t)h * 2 * g.ntile * 128 + t.z + row;      // [H][2][padded rows]
-      __half* d0 = om + prow * D;
-      __half* d1 = d0 + (size_t)g.ntile * 128 * D;
-      // this warpgroup's half of the columns
+      // this warpgroup's half of the columns, by way of the tiles' shared memory
+      // (every product and so every copy into it is done)
+      constexpr int CH = D / 16, BUF = 32 * CH * 16;
+      uint8_t* buf = sm + (warp - 4) * 3 * BUF;
 #pragma unroll 1
       for (int c = m * (D / 64); c < (m + 1) * (D / 64); ++c) {
         uint32_t a[32], b[32];
@@ -387,26 +397,33 @@ k_diff_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         tmem_ld32(tbase + la + 384 + 32 * c, b);
         tmem_wait_ld_regs(a);
         reg_fence32(b);
-        if (in) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 both, u, w;
-            uint32_t *pb = &both.x, *pu = &u.x, *pw = &w.x;
+        for (int e = 0; e < 32; e += 8) {
+          uint4 both, u, w;
+          uint32_t *pb = &both.x, *pu = &u.x, *pw = &w.x;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float x0 = __uint_as_float(a[e + 2 * x]) * i0, x1 = __uint_as_float(a[e + 2 * x + 1]) * i0;
-              const float y0 = __uint_as_float(b[e + 2 * x]) * i1, y1 = __uint_as_float(b[e + 2 * x + 1]) * i1;
-              pb[x] = pack_bf16(fmaf(-lm, y0, x0) * pv, fmaf(-lm, y1, x1) * pv);
-              pu[x] = pack_f16(x0, x1);
-              pw[x] = pack_f16(y0, y1);
-            }
-            *reinterpret_cast<uint4*>(dst + 32 * c + e) = both;
-            if (om) {
-              *reinterpret_cast<uint4*>(d0 + 32 * c + e) = u;
-              *reinterpret_cast<uint4*>(d1 + 32 * c + e) = w;
-            }
+          for (int x = 0; x < 4; ++x) {
+            const float x0 = __uint_as_float(a[e + 2 * x]) * i0, x1 = __uint_as_float(a[e + 2 * x + 1]) * i0;
+            const float y0 = __uint_as_float(b[e + 2 * x]) * i1, y1 = __uint_as_float(b[e + 2 * x + 1]) * i1;
+            pb[x] = pack_bf16(fmaf(-lm, y0, x0) * pv, fmaf(-lm, y1, x1) * pv);
+            pu[x] = pack_f16(x0, x1);
+            pw[x] = pack_f16(y0, y1);
+          }
+          const int piece = 4 * (c - m * (D / 64)) + e / 8;
+          put_piece<CH>(buf, lane, piece, both);
+          if (om) {
+            put_piece<CH>(buf + BUF, lane, piece, u);
+            put_piece<CH>(buf + 2 * BUF, lane, piece, w);
           }
         }
+      }
+      __syncwarp();
+      const int first = t.w * 128 + quarter * 32, live = t.y - first;
+      put_rows<CH>(buf, lane, o + (long long)(t.x + first) * g.ldo + (long long)h * D + m * (D / 2), g.ldo, live);
+      if (om) {
+        __half* d0 = om + ((size_t)h * 2 * g.ntile * 128 + t.z + first) * D + m * (D / 2);
+        put_rows<CH>(buf + BUF, lane, d0, D, live);
+        put_rows<CH>(buf + 2 * BUF, lane, d0 + (size_t)g.ntile * 128 * D, D, live);
       }
       if (lse && in) lse[prow + (size_t)m * g.ntile * 128] = m_run + log2f(l_run) - kPBias;      // base 2
     }

@@ -66,8 +66,9 @@ struct BwdLayout {
   // so there is no slack to align the base in (base_ok checks it).
   static constexpr int VEC = 256;
   static constexpr int HEAD = NA == 2 ? 7168 : 1024;
+  static constexpr int FAC = HEAD - 64;             // [8] float2: the compute warps' factors of the results
   static constexpr int BYTES = HEAD + TILES;
-  static_assert(NA != 2 || VEC + kVecStages * kVecFloats * 4 <= HEAD, "statistics");
+  static_assert(NA != 2 || 64 + VEC + kVecStages * kVecFloats * 4 <= HEAD, "statistics");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -327,18 +328,30 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
-  const int rank = (int)blockIdx.x % g.ntile, hk = (int)blockIdx.x / g.ntile;
-  pdl_start();
-  if (rank >= diff_used(tiles, g, err)) return;
-  if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
-  const DiffTile tl = tiles[rank];
+  int rank, hk;
+  diff_place(g.ok, blockIdx.x, rank, hk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nt = (tl.y + 127) / 128, j = nt - 1 - tl.w;      // early key tiles first: they have the most queries
-  const int per = nt - j, n = per * g.G;                      // query tiles j .. nt - 1 of each head
-  const Powers pw = powers(g, amax, amax_do, lam, seq[rank], hk);
+  if (!base_ok(smem_raw, err)) return;                          // the whole CTA
+  if (threadIdx.x == 0) {
+    prefetch_map(&tk);
+    prefetch_map(&tv);
+    prefetch_map(&tq);
+    prefetch_map(&tdo);
+  }
+  pdl_start();
+  TileLoad ask;
+  ask.ask(tiles, seq, g, rank);
   bwd_setup(bars, warp);
   const uint32_t tbase = bars->tmem_base;
   volatile Abort* ab = &bars->abort;
+  if (!ask.live(g, rank, err)) {                                // the whole CTA
+    if (warp == 1) tmem_dealloc(tbase, 512);
+    return;
+  }
+  const DiffTile tl = tiles[rank];
+  const int nt = (tl.y + 127) / 128, j = nt - 1 - tl.w;      // early key tiles first: they have the most queries
+  const int per = nt - j, n = per * g.G;                      // query tiles j .. nt - 1 of each head
+  const Powers pw = powers(g, amax, amax_do, lam, seq[rank], hk);
   if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0)
@@ -437,6 +450,10 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     const uint32_t cX = tbase + la + kX + 64 * half, cY = tbase + la + kY + 64 * half;
     const float f = pow2f(pw.sh - pw.sp);
     c2 *= pow2f(pw.eq + pw.ek);
+    // the results' factors wait in shared memory, not in registers
+    float2* fac = reinterpret_cast<float2*>(smem_raw + Lay::FAC) + (warp - 4);
+    if (lane == 0) *fac = make_float2(pow2f(pw.edo) * pow2f(-pw.sp), scale * pow2f(pw.edo + pw.ev) * pow2f(pw.eq - pw.sh));
+    __syncwarp();
     bool ok = true;
     int i = j;
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -534,36 +551,40 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->done, 0, ab, err, 51))) {
       tc_fence_after();
       const int key = j * 128 + m;
-      const float mv = pow2f(pw.edo) * pow2f(-pw.sp), mk = scale * pow2f(pw.edo + pw.ev) * pow2f(pw.eq - pw.sh);
-      __nv_bfloat16* ddv = dv + (long long)(tl.x + key) * g.ldv + (long long)hk * D;
-      __nv_bfloat16* ddk = dk + (long long)(tl.x + key) * g.ldk + (long long)hk * D;
+      const float mv = fac->x, mk = fac->y;
+      constexpr int CH = D / 16, BUF = 32 * CH * 16;
+      uint8_t* buf = sm + (warp - 4) * 2 * BUF;           // the operands' memory: all products are done
 #pragma unroll 1
       for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
-        // warp-collective loads: every lane runs them, only the stores are per row
+        // warp-collective loads: every lane runs them
         uint32_t a[32], b[32];
         tmem_ld32(tbase + la + kAcc0 + 32 * c, a);
         tmem_ld32(tbase + la + kAcc1 + 32 * c, b);
         tmem_wait_ld_regs(a);
         reg_fence32(b);
-        if (key < tl.y) {
-          bool fin = true;
+        bool fin = true;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) fin &= fabsf(__uint_as_float(b[e])) < INFINITY;
-          if (!fin) report_error(err, LH_ERR_DEVICE, 101);
+        for (int e = 0; e < 32; ++e) fin &= fabsf(__uint_as_float(b[e])) < INFINITY;
+        if (!fin && key < tl.y) report_error(err, LH_ERR_DEVICE, 101);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 u, w;
-            uint32_t *pu = &u.x, *pw4 = &w.x;
+        for (int e = 0; e < 32; e += 8) {
+          uint4 u, w;
+          uint32_t *pu = &u.x, *pw4 = &w.x;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              pu[x] = pack_bf16(__uint_as_float(a[e + 2 * x]) * mv, __uint_as_float(a[e + 2 * x + 1]) * mv);
-              pw4[x] = pack_bf16(__uint_as_float(b[e + 2 * x]) * mk, __uint_as_float(b[e + 2 * x + 1]) * mk);
-            }
-            *reinterpret_cast<uint4*>(ddv + 32 * c + e) = u;
-            *reinterpret_cast<uint4*>(ddk + 32 * c + e) = w;
+          for (int x = 0; x < 4; ++x) {
+            pu[x] = pack_bf16(__uint_as_float(a[e + 2 * x]) * mv, __uint_as_float(a[e + 2 * x + 1]) * mv);
+            pw4[x] = pack_bf16(__uint_as_float(b[e + 2 * x]) * mk, __uint_as_float(b[e + 2 * x + 1]) * mk);
           }
+          const int piece = 4 * (c - half * (D / 64)) + e / 8;
+          put_piece<CH>(buf, lane, piece, u);
+          put_piece<CH>(buf + BUF, lane, piece, w);
         }
       }
+      __syncwarp();
+      const int first = j * 128 + quarter * 32, live = tl.y - first;
+      const long long col = (long long)hk * D + half * (D / 2);
+      put_rows<CH>(buf, lane, dv + (long long)(tl.x + first) * g.ldv + col, g.ldv, live);
+      put_rows<CH>(buf + BUF, lane, dk + (long long)(tl.x + first) * g.ldk + col, g.ldk, live);
     }
   }
   bwd_teardown(tbase, warp);
@@ -600,20 +621,30 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
   uint8_t* sm = smem_raw + Lay::HEAD;
   float* red = reinterpret_cast<float*>(smem_raw + 256);          // the compute warps' sums of A2 dP
-  const int rank = (int)blockIdx.x % g.ntile, h = (int)blockIdx.x / g.ntile, hk = h / g.G;
-  pdl_start();
-  if (rank >= diff_used(tiles, g, err)) {
-    if (threadIdx.x == 0) part[(size_t)h * g.ntile + rank] = 0.f;
-    return;
-  }
-  if (!base_ok(smem_raw, err)) return;                          // whole CTA, like the line above
-  const DiffTile tl = tiles[rank];
+  int rank, h;
+  diff_place(g.oq, blockIdx.x, rank, h);
+  const int hk = h / g.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = tl.w + 1;
-  const Powers pw = powers(g, amax, amax_do, lam, seq[rank], hk);
+  if (!base_ok(smem_raw, err)) return;                          // the whole CTA
+  if (threadIdx.x == 0) {
+    prefetch_map(&tq);
+    prefetch_map(&tdo);
+    prefetch_map(&tk);
+    prefetch_map(&tv);
+  }
+  pdl_start();
+  TileLoad ask;
+  ask.ask(tiles, seq, g, rank);
   bwd_setup(bars, warp);
   const uint32_t tbase = bars->tmem_base;
   volatile Abort* ab = &bars->abort;
+  if (!ask.live(g, rank, err)) {                                // the whole CTA
+    if (warp == 1) tmem_dealloc(tbase, 512);
+    if (threadIdx.x == 0) part[(size_t)h * g.ntile + rank] = 0.f;
+    return;
+  }
+  const DiffTile tl = tiles[rank];
+  const int n = tl.w + 1;
   if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0) bwd_produce<Lay>(sm, bars, &tq, &tdo, tl.z + tl.w * 128, h, &tk, &tv, tl.z, n, hk, n, ab, err);
@@ -670,11 +701,18 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     const int row = tl.w * 128 + r;
     const size_t rows = (size_t)g.ntile * 128, at = (size_t)h * 2 * rows + tl.z + row;
     const bool in = row < tl.y;
+    const Powers pw = powers(g, amax, amax_do, lam, seq[rank], hk);
     // the first query of a sequence sees one key: f = d = 0 make its dS zero
     const float f = row > 0 ? pow2f(pw.sh - pw.sp) : 0.f, md = -pow2f(-(pw.edo + pw.ev)) * f;
     const float nl1 = in ? (float)pw.sp - lse[at] : 0.f, nl2 = in ? (float)pw.sp - lse[at + rows] : 0.f;
     const float nd1 = in ? delta[at] * md : 0.f, nd2 = in ? delta[at + rows] * md : 0.f;
     c2 *= pow2f(pw.eq + pw.ek);
+    // what the results are multiplied by waits in shared memory, not in registers
+    float2* fac = reinterpret_cast<float2*>(smem_raw + Lay::FAC) + (warp - 4);
+    if (lane == 0)
+      *fac = make_float2(pow2f(pw.edo + pw.ev) * pow2f(-pw.sp),
+                         scale * pow2f(pw.edo + pw.ev) * pow2f(pw.ek - pw.sh) * (half ? -__bfloat162float(lam[h]) : 1.f));
+    __syncwarp();
     float2 dl = make_float2(0.f, 0.f);                    // sum of A2 dP of this thread's columns
     bool ok = true;
     for (int t = 0; t < n; ++t) {
@@ -736,36 +774,38 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
       tc_fence_before();
       mbar_arrive_warp(&bars->ds_ready);
     }
-    float d2 = (dl.x + dl.y) * pow2f(pw.edo + pw.ev) * pow2f(-pw.sp);
+    float d2 = (dl.x + dl.y) * fac->x;
 #pragma unroll
     for (int o = 16; o; o >>= 1) d2 += __shfl_xor_sync(0xffffffffu, d2, o);
     if (lane == 0) red[warp - 4] = d2;
     if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->done, 0, ab, err, 51))) {
       tc_fence_after();
       // dS_2 goes without its factor -lam until here (half 1 holds map 2's columns)
-      const float mq = scale * pow2f(pw.edo + pw.ev) * pow2f(pw.ek - pw.sh) * (half ? -__bfloat162float(lam[h]) : 1.f);
-      __nv_bfloat16* dst = dq + (long long)(tl.x + row) * g.ldq + (long long)h * D;
+      const float mq = fac->y;
+      constexpr int CH = D / 16;
+      uint8_t* buf = sm + (warp - 4) * 32 * CH * 16;      // the operands' memory: all products are done
 #pragma unroll 1
       for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
         uint32_t a[32];
         tmem_ld32(tbase + la + kQAcc + 32 * c, a);
         tmem_wait_ld_regs(a);
-        if (in) {
-          bool fin = true;
+        bool fin = true;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) fin &= fabsf(__uint_as_float(a[e])) < INFINITY;
-          if (!fin) report_error(err, LH_ERR_DEVICE, 101);
+        for (int e = 0; e < 32; ++e) fin &= fabsf(__uint_as_float(a[e])) < INFINITY;
+        if (!fin && in) report_error(err, LH_ERR_DEVICE, 101);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 u;
-            uint32_t* pu = &u.x;
+        for (int e = 0; e < 32; e += 8) {
+          uint4 u;
+          uint32_t* pu = &u.x;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              pu[x] = pack_bf16(__uint_as_float(a[e + 2 * x]) * mq, __uint_as_float(a[e + 2 * x + 1]) * mq);
-            *reinterpret_cast<uint4*>(dst + 32 * c + e) = u;
-          }
+          for (int x = 0; x < 4; ++x)
+            pu[x] = pack_bf16(__uint_as_float(a[e + 2 * x]) * mq, __uint_as_float(a[e + 2 * x + 1]) * mq);
+          put_piece<CH>(buf, lane, 4 * (c - half * (D / 64)) + e / 8, u);
         }
       }
+      __syncwarp();
+      const int first = tl.w * 128 + quarter * 32;
+      put_rows<CH>(buf, lane, dq + (long long)(tl.x + first) * g.ldq + (long long)h * D + half * (D / 2), g.ldq, tl.y - first);
     }
   }
   bwd_teardown(tbase, warp);

@@ -2,6 +2,7 @@
 // Every entry point validates everything before it launches anything, never
 // allocates, never synchronises (except lh_get_device_error) and reports
 // launch failures as LH_ERR_CUDA.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -688,6 +689,10 @@ lh_status make_diff(const lh_diff_config* c, DiffGeom* g, DiffSizes* z) {
   uint32_t tag = 2166136261u;
   for (int v : {c->B, c->T, c->H, c->Hk, c->D, (int)c->dtype, c->packed, c->train, z->tc}) tag = (tag ^ (uint32_t)v) * 16777619u;
   g->tag = (int)tag;
+  const double both = 2.0 * g->ntile * (z->tc ? kDiffTileTC * 2 : kDiffTileFP * 4) * c->D;      // a head's two streamed operands
+  const int grp = (int)std::min<double>(c->Hk, std::max(1.0, kDiffGroupBytes / both));
+  g->oq = diff_order(g->ntile, c->H, grp * g->G);
+  g->ok = diff_order(g->ntile, c->Hk, grp);
   const size_t R = z->tc ? (size_t)g->ntile * kDiffTileTC : T, Hk = c->Hk;     // rows of the statistics
   size_t at = 0;
   auto part = [&at](size_t bytes) { const size_t p = at; at += up256(bytes); return p; };
