@@ -23,8 +23,13 @@
 // the time. Then a cluster of up to 8 blocks shares one tile (split_of): block r
 // takes every r-th tile of the walk, leaves its sums in its shared memory, and
 // each block adds up an equal share of the rows from all of them, in rank order
-// (forward pass: after scaling to the common maximum). 1,021 tokens of 4 heads of
-// 64, forward and backward: 464 us without, 242 us with.
+// (forward pass: after scaling to the common maximum).
+//
+// D = 64 keeps two blocks on an SM (128 registers, a few spilled: dk/dv of 1,021
+// tokens x 4 heads 105 -> 69 us), and the next tile is on its way while what
+// needs the other operand is computed. Forward and backward, 1,021 tokens x 4 heads
+// of 64: 186 us; 2 x 4,096 tokens x 8 heads of 64: 5.26 ms, 46 % of the FMA rate (6.51
+// with one block and no copies ahead).
 #include <cooperative_groups.h>
 
 #include "k_diff.cuh"
@@ -40,11 +45,12 @@ constexpr int kMaxSplit = 8;
 
 namespace cg = cooperative_groups;
 
-// Blocks per tile: enough for two on every SM, no more than the longest walk has
-// tiles.
-int split_of(long long blocks, long long T) {
+// Blocks per tile: as many as the GPU holds at once (two on an SM with D = 64, one
+// with D = 128), no more than the longest walk has tiles. 1,021 tokens x 4 heads of
+// 64 (68 tiles): 267, 188, 198 us with 2, 4, 8.
+int split_of(int D, long long blocks, long long T) {
   int s = 1;
-  while (s < kMaxSplit && blocks * s < 2 * 148 && 2 * s * TS <= T + TS) s *= 2;
+  while (s < kMaxSplit && 2 * s * blocks <= (D == 64 ? 2 : 1) * 148 && 2 * s * TS <= T + TS) s *= 2;
   return s;
 }
 
@@ -91,6 +97,27 @@ __device__ __forceinline__ void stage(float* sm, const T* src, long long ld, int
     d[0] = make_float4(x[0], x[1], x[2], x[3]);
     d[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
+}
+
+// The same, started for fp32 rows (finished by staged()): the walks ask for a tile
+// as soon as its place is free, and do what needs the other operand meanwhile.
+template <typename T, int D>
+__device__ __forceinline__ void stage_ahead(float* sm, const T* src, long long ld, int r0, int end) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int n = 0; n < TS * (D / 4) / NT; ++n) {
+      const int i = threadIdx.x + n * NT, r = i / (D / 4), c = (i - r * (D / 4)) * 4, in = r0 + r < end;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(sm + r * (D + 4) + c)),
+                   "l"(src + (in ? (long long)(r0 + r) * ld + c : 0)), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+  } else {
+    stage<T, D>(sm, src, ld, r0, end);
+  }
+}
+__device__ __forceinline__ void staged() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 }
 
 // acc[i][j] += sum over K columns of A[ty*4+i][.] B[tx+16j][.]
@@ -174,7 +201,7 @@ __device__ __forceinline__ void put(T* row, int tx, const float (&v)[W]) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* __restrict__ q, const T* __restrict__ k,
+__global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) k_diff_fwd_fp(const DiffGeom g, const T* __restrict__ q, const T* __restrict__ k,
                                                     const T* __restrict__ v, const void* lam, const DiffTile* tiles,
                                                     T* __restrict__ o, float* __restrict__ om, float* __restrict__ lse,
                                                     int split, int* err) {
@@ -203,11 +230,10 @@ __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* _
 #pragma unroll
       for (int c = 0; c < W; ++c) acc[u][i][c] = 0.f;
     }
+  if (rank * TS <= r0) stage_ahead<T, D>(K, kb, g.ldk, rank * TS, t.y);
   for (int n0 = rank * TS; n0 <= r0; n0 += split * TS) {
-    __syncthreads();
-    stage<T, D>(K, kb, g.ldk, n0, t.y);
-    stage<T, D>(V, vb, g.ldv, n0, t.y);
-    __syncthreads();
+    staged();                                           // K; nobody reads V any more
+    stage_ahead<T, D>(V, vb, g.ldv, n0, t.y);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float s[4][4] = {};
@@ -235,7 +261,8 @@ __global__ void __launch_bounds__(NT) k_diff_fwd_fp(const DiffGeom g, const T* _
         for (int c = 0; c < W; ++c) acc[u][i][c] *= al;
       }
     }
-    __syncwarp();        // a warp's 8 rows of P are its own
+    staged();            // V; nobody reads K any more (a warp's 8 rows of P are its own)
+    if (n0 + split * TS <= r0) stage_ahead<T, D>(K, kb, g.ldk, n0 + split * TS, t.y);
 #pragma unroll
     for (int u = 0; u < 2; ++u) mm_nn<W, LD>(P + u * TS * LP, V, ty, tx, acc[u]);
   }
@@ -355,7 +382,7 @@ __global__ void __launch_bounds__(256) k_diff_delta_fp(const DiffGeom g, const T
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __restrict__ dout, const T* __restrict__ q,
+__global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) k_diff_dq_fp(const DiffGeom g, const T* __restrict__ dout, const T* __restrict__ q,
                                                    const T* __restrict__ k, const T* __restrict__ v, const void* lam,
                                                    const DiffTile* tiles, const float* __restrict__ lse,
                                                    const float* __restrict__ delta, T* __restrict__ dq, int split, int* err) {
@@ -385,13 +412,14 @@ __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __
       ls[u][i] = r < t.y ? lse[at] : 0.f;
       dl[u][i] = r < t.y ? delta[at] : 0.f;
     }
+  if (rank * TS <= r0) stage_ahead<T, D>(V, vb, g.ldv, rank * TS, t.y);
   for (int n0 = rank * TS; n0 <= r0; n0 += split * TS) {
-    __syncthreads();
-    stage<T, D>(K, kb, g.ldk, n0, t.y);
-    stage<T, D>(V, vb, g.ldv, n0, t.y);
-    __syncthreads();
+    staged();                                           // V; nobody reads K any more
+    stage_ahead<T, D>(K, kb, g.ldk, n0, t.y);
     float dp[4][4] = {};
     mm_nt<D, LD>(O, V, ty, tx, dp);
+    staged();                                           // K; nobody reads V any more
+    if (n0 + split * TS <= r0) stage_ahead<T, D>(V, vb, g.ldv, n0 + split * TS, t.y);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float s[4][4] = {};
@@ -441,7 +469,7 @@ __global__ void __launch_bounds__(NT) k_diff_dq_fp(const DiffGeom g, const T* __
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* __restrict__ dout,
+__global__ void __launch_bounds__(NT, D == 64 ? 2 : 1) k_diff_dkdv_fp(const DiffGeom g, const T* __restrict__ dout,
                                                      const T* __restrict__ q, const T* __restrict__ k,
                                                      const T* __restrict__ v, const void* lam, const DiffTile* tiles,
                                                      const float* __restrict__ lse, const float* __restrict__ delta,
@@ -464,25 +492,31 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
   {
     // the query tiles from this one on, of every head that shares the key head
     const int per = ntl - jt;
+    auto ahead = [&](int it) {
+      const int h = hk * g.G + it / per, i0 = k0 + (it % per) * TS;
+      stage_ahead<T, D>(Q, q + (long long)t.x * g.ldq + (long long)h * D, g.ldq, i0, t.y);
+      // the queries' statistics: lse of both maps, then d of both
+      const int u = threadIdx.x >> 6, c = threadIdx.x & 63, in = i0 + c < t.y;
+      const long long at = (2LL * h + (u & 1)) * g.T + t.x + i0 + c;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(vec + threadIdx.x)),
+                   "l"((u < 2 ? lse : delta) + (in ? at : 0)), "r"(in ? 4 : 0)
+                   : "memory");
+    };
+    if (rank < per * g.G) ahead(rank);
     for (int it = rank; it < per * g.G; it += split) {
       const int h = hk * g.G + it / per, i0 = k0 + (it % per) * TS;
       const float la = lam_of(lam, h, q);
-      __syncthreads();
-      stage<T, D>(Q, q + (long long)t.x * g.ldq + (long long)h * D, g.ldq, i0, t.y);
-      stage<T, D>(O, dout + (long long)t.x * g.ldo + (long long)h * D, g.ldo, i0, t.y);
-      {
-        // the queries' statistics: lse of both maps, then d of both
-        const int u = threadIdx.x >> 6, c = threadIdx.x & 63;
-        const long long at = (2LL * h + (u & 1)) * g.T + t.x + i0 + c;
-        vec[threadIdx.x] = i0 + c < t.y ? (u < 2 ? lse : delta)[at] : 0.f;
-      }
-      __syncthreads();
+      staged();                                         // Q; nobody reads O any more
+      stage_ahead<T, D>(O, dout + (long long)t.x * g.ldo + (long long)h * D, g.ldo, i0, t.y);
       float dp[4][4] = {}, p[4][4];
-      mm_nt<D, LD>(V, O, ty, tx, dp);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float s[4][4] = {};
         mm_nt<DM, LD>(K + u * DM, Q + u * DM, ty, tx, s);
+        if (u == 0) {
+          staged();                                     // O
+          mm_nt<D, LD>(V, O, ty, tx, dp);
+        }
         const float f = u ? -la : 1.f;
         __syncwarp();        // the tile's earlier use of S
 #pragma unroll
@@ -498,7 +532,8 @@ __global__ void __launch_bounds__(NT) k_diff_dkdv_fp(const DiffGeom g, const T* 
         __syncwarp();
         mm_nn<W, LD>(S, Q + u * DM, ty, tx, aK[u]);
       }
-      __syncwarp();
+      __syncthreads();                                  // nobody reads Q any more
+      if (it + split < per * g.G) ahead(it + split);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -568,7 +603,7 @@ cudaError_t fwd_t(const DiffGeom& g, const void* q, const void* k, const void* v
   auto kern = k_diff_fwd_fp<T, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
   if (e != cudaSuccess) return e;
-  return launch_split(kern, g.ntile, g.H, split_of((long long)g.ntile * g.H, g.T), sm, err, s, g, (const T*)q, (const T*)k, (const T*)v, lam,
+  return launch_split(kern, g.ntile, g.H, split_of(D, (long long)g.ntile * g.H, g.T), sm, err, s, g, (const T*)q, (const T*)k, (const T*)v, lam,
                       tiles, (T*)o, om, lse);
 }
 
@@ -583,10 +618,10 @@ cudaError_t bwd_t(const DiffGeom& g, const void* dout, const void* q, const void
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, sm2);
   if (e != cudaSuccess) return e;
-  e = launch_split(kk, g.ntile, g.Hk, split_of((long long)g.ntile * g.Hk, (long long)g.T * g.G), sm2, err, s, g, (const T*)dout, (const T*)q,
+  e = launch_split(kk, g.ntile, g.Hk, split_of(D, (long long)g.ntile * g.Hk, (long long)g.T * g.G), sm2, err, s, g, (const T*)dout, (const T*)q,
                    (const T*)k, (const T*)v, lam, tiles, lse, delta, (T*)dk, (T*)dv);
   if (e != cudaSuccess) return e;
-  return launch_split(kq, g.ntile, g.H, split_of((long long)g.ntile * g.H, g.T), sm1, err, s, g, (const T*)dout, (const T*)q, (const T*)k,
+  return launch_split(kq, g.ntile, g.H, split_of(D, (long long)g.ntile * g.H, g.T), sm1, err, s, g, (const T*)dout, (const T*)q, (const T*)k,
                       (const T*)v, lam, tiles, lse, delta, (T*)dq);
 }
 
