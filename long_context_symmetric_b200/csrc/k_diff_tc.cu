@@ -31,12 +31,14 @@
 // the rows' denominators and each combines half of the columns.
 // Per 128 x 128 pair of tiles: 768 * 16,384 flops against 32,768 exponentials,
 // 1,536 tensor cycles against 2,048 of the special-function unit: it is the
-// exponentials that bound it. Measured at 16 heads of 8,192 tokens, D = 128: 431 us,
-// 955 TFLOP/s, 3,110 cycles per pair (score wait 1,100, loads and maximum 420,
+// exponentials that bound it. Measured at 16 heads of 8,192 tokens, D = 128: 397 us,
+// 1,037 TFLOP/s, and 10 us per CTA besides the pairs; 3,110 cycles per pair (score wait 1,100, loads and maximum 420,
 // exponentials 1,400 per map, the two maps half a turn apart). Slower: keys in
 // halves of 64 with two score buffers per map (the N = 64 score products cost more
 // than the waits they hide), an issuer per map, a share of the exponentials as
-// polynomials on the FMA pipe.
+// polynomials on the FMA pipe; for D = 64, P behind O in tensor memory and the next
+// scores formed as soon as the warps hold these (412 against 386 us: without the
+// wait both maps' warps meet in the exponentials).
 #include <cudaTypedefs.h>
 
 #include "k_diff_tc.cuh"
