@@ -331,3 +331,20 @@ def test_without_gradients_nothing_is_kept_for_them(dtype, monkeypatch):
     c.backward(do[None])
     assert [m.train for m in made] == [0, 0, 1]
     assert torch.equal(a, b) and torch.equal(a, c.detach()) and lh.get_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,G", [("fp32", 1), ("bf16", 1), ("bf16", 2)])
+def test_heads_that_do_not_fit_l2_together(dtype, G):
+    """400 sequences of 200 tokens: the tiles of three key/value heads are taken in more than one group. Each head by
+    itself gives the same bits."""
+    B, N, Hk, D = 400, 200, 3, 64
+    q, k, v, lam, do = inputs(171, B * N, Hk * G, Hk, D, dtype)
+    got = run(lh.make_diff_config(B, N, Hk * G, D, dtype, Hk), q, k, v, lam, do)
+    one = lh.make_diff_config(B, N, G, D, dtype, 1)
+    for h in range(Hk):
+        heads, kv = slice(h * G, h * G + G), slice(h, h + 1)
+        ref = run(one, q[:, heads].contiguous(), k[:, kv].contiguous(), v[:, kv].contiguous(), lam[heads].clone(),
+                  do[:, heads].contiguous())
+        for n, at in (("o", heads), ("dq", heads), ("dk", kv), ("dv", kv)):
+            assert torch.equal(got[n][:, at], ref[n]), (n, h)
+        assert torch.equal(got["dlam"][heads], ref["dlam"])
