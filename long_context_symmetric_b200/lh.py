@@ -22,6 +22,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "lh.h")
 
 LH_BF16, LH_FP32 = 0, 1
 LH_ACC_FP32, LH_ACC_FIXED64 = 0, 1
+LH_ERR_NULL = 1
 MAX_LEVELS = 8
 MAX_K = 4096
 
@@ -437,7 +438,11 @@ def _call(name, dev, stream, *args):
     """One entry point, on the device that the tensors live on."""
     f = getattr(_lib or lib(), name)
     if dev.type != "cuda":
-        st = f(*args, _stream(stream))
+        # host memory never reaches a kernel: asked without pointers, the library
+        # names what is wrong with the configuration and launches nothing
+        st = f(*(None if t is c_void_p else a for a, t in zip((*args, None), f.argtypes)))
+        if st in (0, LH_ERR_NULL):
+            raise ValueError(f"{name}: the tensors are on {dev}, a CUDA device is wanted")
     elif dev.index == _raw_device():
         st = f(*args, _raw_stream(dev.index) if stream is None else _stream(stream))
     else:
