@@ -31,6 +31,8 @@
 // Rows of odd length, or whose stride is no multiple of 8 elements, are read
 // element by element with the columns dealt out to neighbouring lanes (VEC =
 // false), which keeps the accesses of a warp contiguous.
+#include <atomic>
+
 #include "lh_common.cuh"
 
 namespace lh {
@@ -528,8 +530,17 @@ cudaError_t bwd_t(const NormShape& s, const NormArgs& a, int nb, cudaStream_t st
               : s.nv == 1 ? k_norm_bwd<T, VEC, 0, 1, RB, true>
               : s.nv == 2 ? k_norm_bwd<T, VEC, 0, 2, 1, true>
                           : k_norm_bwd<T, VEC, 0, 4, 1, false>;
-  if (sm > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (s.nv == 4) {
+    // The attribute belongs to the kernel on its device, not to this call: it is set
+    // once, to what the longest row needs, so that no call takes back what another
+    // host thread's is about to launch with.
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(dev < 64 && (done.load() >> dev & 1))) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * LH_NORM_MAX_D * 4);
+      if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    }
     if (e != cudaSuccess) return e;
   }
   kern<<<nb, s.threads, sm, st>>>(a);

@@ -1,5 +1,8 @@
 """Layer norm, forward and backward, against its 64-bit form."""
 
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -185,3 +188,35 @@ def test_offsets_past_32_bits():
     lh.norm_fwd(lh.make_norm_config(M, d, ldx=ld), far, w, None, b)
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+def test_two_host_threads_with_rows_of_unlike_length():
+    """Rows of more than 8,192 values keep their columns' sums in shared memory, as much as their length takes: calls of
+    two lengths from two host threads at once do not get in each other's way. (The C function itself: the binding's own
+    work between two calls would keep the threads apart.)"""
+    f, keep = lh.lib().lh_norm_bwd, []
+
+    def job(d):
+        x, dy, w = rand(1, 2, d, dtype="bf16"), rand(2, 2, d, dtype="bf16"), rand(3, d, dtype="bf16")
+        cfg, one = lh.make_norm_config(2, d), torch.ones(2, device=DEV)
+        ts = (dy, x, w, one, one, torch.empty_like(x), torch.empty_like(w), torch.empty_like(w), lh.norm_workspace(cfg, DEV))
+        stream = torch.cuda.Stream()
+        keep.append((cfg, ts, stream))
+        return ctypes.byref(cfg), *(t.data_ptr() for t in ts), ts[-1].numel(), stream.cuda_stream
+
+    jobs = [job(16384), job(8200)]
+    states, go = [set(), set()], threading.Barrier(len(jobs))
+    torch.cuda.synchronize()
+
+    def loop(args, seen):
+        go.wait()
+        for _ in range(20000):
+            seen.add(f(*args))
+
+    threads = [threading.Thread(target=loop, args=a) for a in zip(jobs, states)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert states == [{0}, {0}]
