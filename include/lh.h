@@ -497,7 +497,9 @@ lh_status lh_diff_plan(const lh_diff_config* cfg, lh_diff_plan_t* out);
  * bounds); sequences may be empty; rows outside [cu[0], cu[B]) are neither
  * read nor written, and a sequence's rows are read for that sequence alone.
  * packed = 0: cu is NULL. bf16 I/O runs on the tensor cores (fp16 operands
- * with a power of two per sequence and head, as in lh_attn_fwd; a non-finite
+ * with a power of two per sequence and key/value head, as in lh_attn_fwd: a
+ * value of q, k or v 2^-14 and less of the largest one may lose bits, down to
+ * 2^-22 of it; a non-finite
  * value is reported, LH_ERR_DEVICE detail 102), fp32 in fp32 arithmetic. A
  * non-finite k or v value may reach every row of its sequence and head (0 times
  * it is not 0), no other. */
@@ -507,7 +509,11 @@ lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void*
 /* Gradients of lh_diff_attn_fwd (cfg->train = 1, same cfg, inputs and
  * saved; a buffer that no forward pass of this problem wrote is reported,
  * LH_ERR_DEVICE detail 404, and not followed): dq, dk, dv (rows outside the
- * sequences are not written) and dlam [H]. Deterministic, shared heads included (no atomics). */
+ * sequences are not written) and dlam [H]. Deterministic, shared heads included (no atomics).
+ * bf16: every row of dout has a power of two of its own, so a dq row is as
+ * accurate as its own size allows; what a query adds to a key's dk and dv is
+ * rounded at 2^-38 and more below what the largest row that sees the key's tile
+ * could add. */
 lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const void* q, const void* k, const void* v,
                            const void* lam, const int32_t* cu, const void* saved, size_t saved_bytes,
                            void* ws, size_t ws_bytes, void* dq, void* dk, void* dv, void* dlam, void* stream);

@@ -20,9 +20,10 @@ struct DiffTC {
   __half *qs, *ks, *vs;       // [H | Hk][padded rows][D]
   __half* om;                 // [H][2][padded rows][D]: A_m v 2^-ev
   float* lse;                 // [H][2][padded rows], base 2
-  uint32_t* amax_do;          // [B][Hk], like q's
-  __half* dos;                // [H][padded rows][D]
-  float* delta;               // [H][2][padded rows]
+  int* rowx;                  // [H][padded rows]: row_word of each row of do
+  int* tmax;                  // [H][padded tiles]: the largest of both parts in the tile
+  __half* dos;                // [H][padded rows][D]: do 2^-e, e of the row
+  float* delta;               // [H][2][padded rows]: d_m 2^-(e + ev)
   float* part;                // [H][ntile] sums of A2 dP
 };
 
@@ -35,6 +36,13 @@ __host__ __device__ __forceinline__ int diff_exp(uint32_t amax_bits) {
   const int ex = (int)((amax_bits >> 23) & 0xFFu) - 127;
   return ex >= -3 && ex < 2 ? 0 : scale_exp(amax_bits);
 }
+
+// A row of do: the exponent e of its copy, and x with |row|_1 < 2^x; kRowNone
+// where it has nothing to say.
+constexpr int kRowNone = -1000;
+__device__ __forceinline__ int row_word(int e, int x) { return (int)((unsigned)x << 16 | ((unsigned)e & 0xFFFFu)); }
+__device__ __forceinline__ int row_e(int w) { return (short)(w & 0xFFFF); }
+__device__ __forceinline__ int row_x(int w) { return w >> 16; }
 
 // Registers. A CTA of three warpgroups (384 threads) is launched with 168
 // registers a thread, all that a one-CTA SM has (launch bounds 384, 1). The

@@ -8,15 +8,28 @@
 // A query that sees one key has A = 1 and dS = 0 exactly; its dS is set to zero
 // rather than left to the rounding of dP - d.
 //
-// Ranges. The maps are held at 2^sp (1 + |lam| below 2^(14 - sp)), dS at 2^sh
-// with sh from the largest v and do: |dP - d| <= 2 D max|v| max|do|, so that no
-// dS leaves fp16 whatever the data, and an average one (A of 1 / n) stays
-// normal. The powers are taken out of the fp32 results.
+// Ranges. Gradients of one sequence differ by many powers of two from row to row,
+// so every row of do is copied times a power of its own, 2^-e, which leaves the
+// row's products as a factor. The maps are held at 2^sp (1 + |lam| below
+// 2^(14 - sp)), dS at 2^sh from the bound |dP - d| <= 2 |do row|_1 max |v|:
+// no dS leaves fp16 whatever the data.
+// - dq: a query row is a lane, so sh and e are the row's own: a dS is normal
+//   down to 2^-29 of that bound, and neither another row's do nor its place in the
+//   sequence matters.
+// - dk, dv: the rows of all queries that see a key tile enter one sum. E is the
+//   largest e of that walk and sh from its largest row; A enters times
+//   2^(sp + e - E), so that A dos and A (dP - d) come out at one power. What a row
+//   adds there keeps its bits down to 2^-29 of the walk's bound (dk) and to 2^-27
+//   of its largest do (dv); below, it is off by 2^-40 and 2^-38 of them at most.
+//   The keys that only small rows see are another walk with its own E.
+// (Before, one power per sequence and head from 2 D max |v| max |do|: dq rows whose
+// do was 2^-14 of the largest were off by 3 % after 8,192 keys with one v of 100.)
+// The powers are taken out of the fp32 results.
 //
-// k_diff_pack_do copies do like the forward's working copies and forms d1, d2 in
-// the same pass. (The sum of d2 that dlam needs is formed as the sum of A2 dP in
-// the dq kernel, from fp32 values: a sum over a long sequence can be small beside
-// its terms, and the saved outputs' 11 bits would show in it.)
+// k_diff_pack_do copies do and forms d1, d2 in the same pass, both in the copy's
+// units (times 2^-(e + ev)). (The sum of d2 that dlam needs is formed as the sum of
+// A2 dP in the dq kernel, from fp32 values: a sum over a long sequence can be small
+// beside its terms, and the saved outputs' 11 bits would show in it.)
 //
 // k_diff_dkdv_tc: one CTA per key tile and key/value head, over the query tiles
 // from its own on, of every query head that shares it. Work per pair of tiles:
@@ -62,11 +75,13 @@ struct BwdLayout {
   static constexpr int FIX0 = 0, FIX1 = OPB, RA = 2 * OPB, RB = RA + NSTA * OPB;
   static constexpr int TILES = RB + NSTB * OPB;
   // barriers, the queries' statistics (NA = 2), up to the next 1,024-byte
-  // boundary. With three stages of D = 128 that is all of a CTA's shared memory,
-  // so there is no slack to align the base in (base_ok checks it).
+  // boundary. With three stages of D = 128 that leaves 1,024 bytes of a CTA's shared
+  // memory: the base is not aligned here but has to be (base_ok checks it).
   static constexpr int VEC = 256;
-  static constexpr int HEAD = NA == 2 ? 7168 : 1024;
-  static constexpr int FAC = HEAD - 64;             // [8] float2: the compute warps' factors of the results
+  static constexpr int HEAD = NA == 2 ? 7168 : 2048;
+  // the walk's WalkScale (NA = 2), or a float4 of each compute warp's factors and
+  // behind them 2^e of each compute thread's row (NA = 3)
+  static constexpr int FAC = NA == 2 ? HEAD - 64 : 1024 - kComputeWarps * 16;
   static constexpr int BYTES = HEAD + TILES;
   static_assert(NA != 2 || 64 + VEC + kVecStages * kVecFloats * 4 <= HEAD, "statistics");
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -83,24 +98,46 @@ static_assert(sizeof(BwdBars) <= 256, "barrier block");
 
 // Powers of two of one sequence and key/value head.
 struct Powers {
-  int eq, ek, ev, edo, sp, sh;
+  int eq, ek, ev, sp;
+  int vx;                     // the v copy is below 2^vx
+  int ll;                     // |lam| <= 2^ll, ll >= 0
 };
-__device__ __forceinline__ Powers powers(const DiffGeom& g, const uint32_t* amax, const uint32_t* amax_do,
-                                         const __nv_bfloat16* lam, int b, int hk) {
+__device__ __forceinline__ Powers powers(const DiffGeom& g, const uint32_t* amax, const __nv_bfloat16* lam, int b, int hk) {
   const size_t plane = (size_t)g.B * g.Hk, at = (size_t)b * g.Hk + hk;
-  const uint32_t av = amax[kScaleV * plane + at], ad = amax_do[at];
+  const uint32_t av = amax[kScaleV * plane + at];
   Powers p;
   p.eq = diff_exp(amax[kScaleQ * plane + at]);
   p.ek = diff_exp(amax[kScaleK * plane + at]);
   p.ev = diff_exp(av);
-  p.edo = diff_exp(ad);
+  p.vx = (int)(av >> 23) - 126 - p.ev;
   float lm = 0.f;
   for (int h = hk * g.G; h < (hk + 1) * g.G; ++h) lm = fmaxf(lm, fabsf(__bfloat162float(lam[h])));
-  p.sp = max(-100, 13 - ilogbf(1.f + fminf(lm, 1e30f)));
-  const float bound = 2.f * (float)g.D * (__uint_as_float(av) * pow2f(-p.ev)) * (__uint_as_float(ad) * pow2f(-p.edo)) *
-                      fminf(fmaxf(1.f, lm), 1e20f);
-  p.sh = bound > 1e-30f && bound < 1e38f ? max(-60, min(14, 14 - ilogbf(bound))) : 0;
+  lm = fminf(lm, 1e30f);
+  p.sp = max(-100, 13 - ilogbf(1.f + lm));
+  p.ll = lm > 1.f ? ilogbf(lm) + 1 : 0;
   return p;
+}
+// What a walk of dk, dv is scaled by: f = 2^(sh - sp), the scores' 2^(eq + ek), the
+// results' factors; sp - E.
+struct WalkScale {
+  float f, s, dv, dk;
+  int base;
+};
+// 2^sh for dS of rows (of the do copy) with a 1-norm below 2^xn: |dS| 2^sh < 2^15
+__device__ __forceinline__ int ds_exp(const Powers& p, int xn, int ll) { return max(-60, min(24, 14 - xn - p.vx - ll)); }
+
+// The largest e and the largest exponent of a row's 1-norm over the query tiles of a
+// walk (padded tiles first .. first + per - 1 of the group's heads); a whole warp.
+__device__ __forceinline__ void walk_max(const int* tmax, const DiffGeom& g, int hk, int first, int per, int& E, int& X) {
+  E = X = -32768;
+  for (int h = hk * g.G; h < (hk + 1) * g.G; ++h)
+    for (int i = threadIdx.x & 31; i < per; i += 32) {
+      const int w = tmax[(size_t)h * g.ntile + first + i];
+      E = max(E, row_e(w));
+      X = max(X, row_x(w));
+    }
+  E = max(__reduce_max_sync(0xffffffffu, E), -kScaleMaxExp);      // rows of zeros alone
+  X = __reduce_max_sync(0xffffffffu, X);
 }
 
 // The swizzled tiles need a 1,024-byte aligned base; dynamic shared memory starts
@@ -321,9 +358,9 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
 k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo, const DiffGeom g,
                const __nv_bfloat16* __restrict__ lam, const DiffTile* __restrict__ tiles, const int* __restrict__ seq,
-               const uint32_t* __restrict__ amax, const uint32_t* __restrict__ amax_do, const float* __restrict__ lse,
-               const float* __restrict__ delta, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, float c2,
-               float scale, int* err) {
+               const uint32_t* __restrict__ amax, const int* __restrict__ rowx, const int* __restrict__ tmax,
+               const float* __restrict__ lse, const float* __restrict__ delta, __nv_bfloat16* __restrict__ dk,
+               __nv_bfloat16* __restrict__ dv, float c2, float scale, int* err) {
   using Lay = BwdLayout<D, 2>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem_raw);
@@ -351,7 +388,7 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   const DiffTile tl = tiles[rank];
   const int nt = (tl.y + 127) / 128, j = nt - 1 - tl.w;      // early key tiles first: they have the most queries
   const int per = nt - j, n = per * g.G;                      // query tiles j .. nt - 1 of each head
-  const Powers pw = powers(g, amax, amax_do, lam, seq[rank], hk);
+  WalkScale* ws = reinterpret_cast<WalkScale*>(smem_raw + Lay::FAC);
   if (warp < 4) regs_give();
   if (warp == 0) {
     if (lane == 0)
@@ -406,13 +443,29 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       }
     }
     is.finish(ok);
+  } else if (warp == 3) {
+    // the walk's powers of two, for the warps that need them
+    const Powers pw = powers(g, amax, lam, seq[rank], hk);
+    int E, X;
+    walk_max(tmax, g, hk, (tl.z >> 7) + j, per, E, X);
+    const int sh = ds_exp(pw, X - E, pw.ll);
+    if (lane == 0) {
+      ws->f = pow2f(sh - pw.sp);
+      ws->s = pow2f(pw.eq + pw.ek);
+      ws->dv = pow2f(E) * pow2f(-pw.sp);
+      ws->dk = scale * pow2f(E + pw.ev) * pow2f(pw.eq - sh);
+      ws->base = pw.sp - E;
+    }
+    named_bar_sync(1, 320);              // warps 2 .. 11
   } else if (warp == 2) {
+    named_bar_sync(1, 320);
     // the queries' statistics, a few tiles ahead of the compute warps: [0] -lse 1,
-    // [1] -lse 2 + log2 |lam| (both + sp), [2] -d1, [3] -d2 in dS units and signed
-    // like the map in A1 - lam A2; then that sign. Rows past the end: zeros, so
-    // that dS = 0 there.
+    // [1] -lse 2 + log2 |lam| (both + sp + e - E), [2] -d1, [3] -d2 in dS units and
+    // signed like the map in A1 - lam A2; then that sign. Rows past the end: zeros,
+    // so that dS = 0 there.
     const size_t rows = (size_t)g.ntile * 128;
-    const float f = pow2f(pw.sh - pw.sp), md = -pow2f(-(pw.edo + pw.ev)) * f, fsp = (float)pw.sp;
+    const float md = -ws->f;
+    const int base = ws->base;
     int i = j, h = hk * g.G;
     for (int t = 0; t < n; ++t) {
       const int st = t % kVecStages;
@@ -422,16 +475,19 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       float* vec = reinterpret_cast<float*>(smem_raw + Lay::VEC) + st * kVecFloats;
       const float l = __bfloat162float(lam[h]), sg = l > 0.f ? -1.f : 1.f, ll = log2f(fabsf(l));
       const int q = i * 128 + 4 * lane;
+      const int4 w = *reinterpret_cast<const int4*>(rowx + (size_t)h * rows + tl.z + q);
+      const float4 ad = make_float4((float)(base + row_e(w.x)), (float)(base + row_e(w.y)), (float)(base + row_e(w.z)),
+                                    (float)(base + row_e(w.w)));
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int mp = v & 1;
         const float4 x = *reinterpret_cast<const float4*>((v < 2 ? lse : delta) + ((size_t)h * 2 + mp) * rows + tl.z + q);
-        const float add = fsp + (mp ? ll : 0.f), mul = md * (mp ? sg : 1.f);
+        const float add = mp ? ll : 0.f, mul = md * (mp ? sg : 1.f);
         float4 y;
-        y.x = q < tl.y ? (v < 2 ? add - x.x : x.x * mul) : 0.f;
-        y.y = q + 1 < tl.y ? (v < 2 ? add - x.y : x.y * mul) : 0.f;
-        y.z = q + 2 < tl.y ? (v < 2 ? add - x.z : x.z * mul) : 0.f;
-        y.w = q + 3 < tl.y ? (v < 2 ? add - x.w : x.w * mul) : 0.f;
+        y.x = q < tl.y ? (v < 2 ? ad.x + add - x.x : x.x * mul) : 0.f;
+        y.y = q + 1 < tl.y ? (v < 2 ? ad.y + add - x.y : x.y * mul) : 0.f;
+        y.z = q + 2 < tl.y ? (v < 2 ? ad.z + add - x.z : x.z * mul) : 0.f;
+        y.w = q + 3 < tl.y ? (v < 2 ? ad.w + add - x.w : x.w * mul) : 0.f;
         *reinterpret_cast<float4*>(vec + 128 * v + 4 * lane) = y;
       }
       if (lane == 0) vec[512] = sg;
@@ -448,12 +504,9 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     const int m = quarter * 32 + lane;                  // key row within the tile / TMEM lane
     const uint32_t la = (uint32_t)(quarter * 32) << 16;
     const uint32_t cX = tbase + la + kX + 64 * half, cY = tbase + la + kY + 64 * half;
-    const float f = pow2f(pw.sh - pw.sp);
-    c2 *= pow2f(pw.eq + pw.ek);
-    // the results' factors wait in shared memory, not in registers
-    float2* fac = reinterpret_cast<float2*>(smem_raw + Lay::FAC) + (warp - 4);
-    if (lane == 0) *fac = make_float2(pow2f(pw.edo) * pow2f(-pw.sp), scale * pow2f(pw.edo + pw.ev) * pow2f(pw.eq - pw.sh));
-    __syncwarp();
+    named_bar_sync(1, 320);
+    const float f = ws->f;
+    c2 *= ws->s;
     bool ok = true;
     int i = j;
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -551,7 +604,7 @@ k_diff_dkdv_tc(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->done, 0, ab, err, 51))) {
       tc_fence_after();
       const int key = j * 128 + m;
-      const float mv = fac->x, mk = fac->y;
+      const float mv = ws->dv, mk = ws->dk;
       constexpr int CH = D / 16, BUF = 32 * CH * 16;
       uint8_t* buf = sm + (warp - 4) * 2 * BUF;           // the operands' memory: all products are done
 #pragma unroll 1
@@ -613,7 +666,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
 k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
              const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DiffGeom g,
              const __nv_bfloat16* __restrict__ lam, const DiffTile* __restrict__ tiles, const int* __restrict__ seq,
-             const uint32_t* __restrict__ amax, const uint32_t* __restrict__ amax_do, const float* __restrict__ lse,
+             const uint32_t* __restrict__ amax, const int* __restrict__ rowx, const float* __restrict__ lse,
              const float* __restrict__ delta, __nv_bfloat16* __restrict__ dq, float* __restrict__ part, float c2, float scale,
              int* err) {
   using Lay = BwdLayout<D, 3>;
@@ -701,17 +754,19 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     const int row = tl.w * 128 + r;
     const size_t rows = (size_t)g.ntile * 128, at = (size_t)h * 2 * rows + tl.z + row;
     const bool in = row < tl.y;
-    const Powers pw = powers(g, amax, amax_do, lam, seq[rank], hk);
+    const Powers pw = powers(g, amax, lam, seq[rank], hk);
+    const int rw = in ? rowx[(size_t)h * rows + tl.z + row] : 0;
     // the first query of a sequence sees one key: f = d = 0 make its dS zero
-    const float f = row > 0 ? pow2f(pw.sh - pw.sp) : 0.f, md = -pow2f(-(pw.edo + pw.ev)) * f;
+    const float f = row > 0 ? pow2f(ds_exp(pw, row_x(rw) - row_e(rw), 0) - pw.sp) : 0.f, md = -f;
     const float nl1 = in ? (float)pw.sp - lse[at] : 0.f, nl2 = in ? (float)pw.sp - lse[at + rows] : 0.f;
     const float nd1 = in ? delta[at] * md : 0.f, nd2 = in ? delta[at + rows] * md : 0.f;
     c2 *= pow2f(pw.eq + pw.ek);
     // what the results are multiplied by waits in shared memory, not in registers
-    float2* fac = reinterpret_cast<float2*>(smem_raw + Lay::FAC) + (warp - 4);
+    float4* fac = reinterpret_cast<float4*>(smem_raw + Lay::FAC) + (warp - 4);
+    reinterpret_cast<float*>(smem_raw + 1024)[threadIdx.x - 128] = pow2f(row_e(rw));
     if (lane == 0)
-      *fac = make_float2(pow2f(pw.edo + pw.ev) * pow2f(-pw.sp),
-                         scale * pow2f(pw.edo + pw.ev) * pow2f(pw.ek - pw.sh) * (half ? -__bfloat162float(lam[h]) : 1.f));
+      *fac = make_float4(pow2f(pw.ev), pow2f(-pw.sp),
+                         scale * pow2f(pw.ev) * pow2f(pw.ek) * (half ? -__bfloat162float(lam[h]) : 1.f), 0.f);
     __syncwarp();
     float2 dl = make_float2(0.f, 0.f);                    // sum of A2 dP of this thread's columns
     bool ok = true;
@@ -774,14 +829,16 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
       tc_fence_before();
       mbar_arrive_warp(&bars->ds_ready);
     }
-    float d2 = (dl.x + dl.y) * fac->x;
+    const float pe = reinterpret_cast<const float*>(smem_raw + 1024)[threadIdx.x - 128];
+    float d2 = (dl.x + dl.y) * fac->x * pe * fac->y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) d2 += __shfl_xor_sync(0xffffffffu, d2, o);
     if (lane == 0) red[warp - 4] = d2;
     if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->done, 0, ab, err, 51))) {
       tc_fence_after();
       // dS_2 goes without its factor -lam until here (half 1 holds map 2's columns)
-      const float mq = fac->y;
+      // 2^-sh = 2^-sp / f, a power of two
+      const float mq = f > 0.f ? fac->z * pe * (__int_as_float(0x7F000000 - __float_as_int(f)) * fac->y) : 0.f;
       constexpr int CH = D / 16;
       uint8_t* buf = sm + (warp - 4) * 32 * CH * 16;      // the operands' memory: all products are done
 #pragma unroll 1
@@ -817,79 +874,91 @@ k_diff_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
 }
 
 // ---------------------------------------------------------------- do: working copy, d1, d2
-// One 128-row tile of one head; D / 8 lanes to a row. REDO: the copy alone, for
-// heads whose power is not 2^0.
-template <bool REDO, int D>
+// One 128-row tile of one head; D / 8 lanes to a row.
+template <int D>
 __global__ void __launch_bounds__(256) k_diff_pack_do(const DiffGeom g, const __nv_bfloat16* __restrict__ dout,
                                                       const __half* __restrict__ om, const DiffTile* __restrict__ tiles,
-                                                      const int* __restrict__ seq, const uint32_t* __restrict__ amax,
-                                                      uint32_t* amax_do, __half* __restrict__ dos,
-                                                      float* __restrict__ delta, int* err) {
+                                                      __half* __restrict__ dos, float* __restrict__ delta,
+                                                      int* __restrict__ rowx, int* __restrict__ tmax, int* err) {
   constexpr int L = D / 8, RPB = 256 / L;      // lanes per row, rows per step
-  const int h = blockIdx.y, hk = h / g.G, lane = threadIdx.x & 31;
-  if (REDO) pdl_start();
+  __shared__ int red[2][8];
+  const int h = blockIdx.y, lane = threadIdx.x & 31;
+  pdl_start();
   if ((int)blockIdx.x >= diff_used(tiles, g, err)) return;
   const DiffTile t = tiles[blockIdx.x];
-  const size_t sh = (size_t)seq[blockIdx.x] * g.Hk + hk;
-  float mul = 1.f;
-  if (REDO) {
-    const int e = diff_exp(amax_do[sh]);
-    if (e == 0) return;
-    mul = pow2f(-e);
-  }
   const int r0 = t.w * 128, c = (threadIdx.x % L) * 8;
   const size_t rows = (size_t)g.ntile * 128;
-  const float pv = REDO ? 1.f : pow2f(diff_exp(amax[(size_t)kScaleV * g.B * g.Hk + sh]));
-  uint32_t mx = 0;
+  int E = kRowNone, X = kRowNone;
+  bool fin = true;
 #pragma unroll 2
   for (int r = threadIdx.x / L; r < 128; r += RPB) {
     const bool in = r0 + r < t.y;
     const size_t prow = (size_t)t.z + r0 + r;
     uint4 raw = make_uint4(0, 0, 0, 0);
-    if (in) raw = __ldg(reinterpret_cast<const uint4*>(dout + (long long)(t.x + r0 + r) * g.ldo + (long long)h * D + c));
-    const __nv_bfloat162* hb = reinterpret_cast<const __nv_bfloat162*>(&raw);
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = __bfloat1622float2(hb[e]);
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
+    float u[8] = {}, w[8] = {};
+    if (in) {
+      raw = __ldg(reinterpret_cast<const uint4*>(dout + (long long)(t.x + r0 + r) * g.ldo + (long long)h * D + c));
+      Vec8<__half>::load_f32(om + ((size_t)h * 2 * rows + prow) * D + c, u);
+      Vec8<__half>::load_f32(om + ((size_t)(h * 2 + 1) * rows + prow) * D + c, w);
     }
-    if (!REDO) {
-      mx = max(mx, absmax8_bf16(raw));
-      float a = 0.f, b = 0.f;
-      if (in) {
-        float u[8], w[8];
-        Vec8<__half>::load_f32(om + ((size_t)h * 2 * rows + prow) * D + c, u);
-        Vec8<__half>::load_f32(om + ((size_t)(h * 2 + 1) * rows + prow) * D + c, w);
+    uint32_t mx = absmax8_bf16(raw);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a = fmaf(x[e], u[e], a);
-          b = fmaf(x[e], w[e], b);
-        }
-      }
+    for (int o = L / 2; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    fin = fin && mx < 0x7F800000u;
+    // a row of zeros, or one that is not finite, asks for nothing of the others
+    const bool some = mx != 0 && mx < 0x7F800000u;
+    const int e = some ? diff_exp(mx) : -kScaleMaxExp;
+    const float mul = pow2f(-e);
+    const __nv_bfloat162* hb = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    float x[8], a = 0.f, b = 0.f, ss = 0.f;
 #pragma unroll
-      for (int o = L / 2; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-      }
-      if (threadIdx.x % L == 0) {
-        delta[(size_t)h * 2 * rows + prow] = a * pv;
-        delta[(size_t)(h * 2 + 1) * rows + prow] = b * pv;
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __bfloat1622float2(hb[k]);
+      x[2 * k] = f.x * mul;
+      x[2 * k + 1] = f.y * mul;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      a = fmaf(x[k], u[k], a);
+      b = fmaf(x[k], w[k], b);
+      ss += fabsf(x[k]);
+    }
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
+    const int nx = some ? e + (int)(__float_as_uint(ss) >> 23) - 126 : kRowNone;
+    if (in && some) {
+      E = max(E, e);
+      X = max(X, nx);
+    }
+    if (threadIdx.x % L == 0) {
+      delta[(size_t)h * 2 * rows + prow] = a;
+      delta[(size_t)(h * 2 + 1) * rows + prow] = b;
+      rowx[(size_t)h * rows + prow] = row_word(e, nx);
     }
     uint4 out;
     uint32_t* po = &out.x;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) po[e] = pack_f16(x[2 * e] * mul, x[2 * e + 1] * mul);
+    for (int k = 0; k < 4; ++k) po[k] = pack_f16(x[2 * k], x[2 * k + 1]);
     *reinterpret_cast<uint4*>(dos + ((size_t)h * rows + prow) * D + c) = out;
   }
-  if (!REDO) {
-    const bool fin = mx < 0x7F800000u;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0 && mx > amax_do[sh]) atomicMax(amax_do + sh, mx);
-    if (!fin) report_error(err, LH_ERR_DEVICE, 102);
+  if (!fin) report_error(err, LH_ERR_DEVICE, 102);
+  E = __reduce_max_sync(0xffffffffu, E);
+  X = __reduce_max_sync(0xffffffffu, X);
+  if (lane == 0) {
+    red[0][threadIdx.x >> 5] = E;
+    red[1][threadIdx.x >> 5] = X;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 8; ++k) {
+      E = max(E, red[0][k]);
+      X = max(X, red[1][k]);
+    }
+    tmax[(size_t)h * g.ntile + (t.z >> 7) + t.w] = row_word(E, X);
   }
 }
 
@@ -910,26 +979,21 @@ cudaError_t bwd_t(const DiffGeom& g, const DiffTC& b, const void* dout, const vo
   const float c2 = (float)(1.4426950408889634 / sqrt((double)(D / 2)));
   const dim3 gp(g.ntile, g.H);
   const __nv_bfloat16 *L = (const __nv_bfloat16*)lam, *dO = (const __nv_bfloat16*)dout;
-  k_diff_pack_do<false, D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta, err);
+  k_diff_pack_do<D><<<gp, 256, 0, s>>>(g, dO, b.om, b.tiles, b.dos, b.delta, b.rowx, b.tmax, err);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_next(k_diff_pack_do<true, D>, gp, 256, 0, s, g, dO, b.om, b.tiles, b.seq, b.amax, b.amax_do, b.dos, b.delta,
-                  err);
-  if (e != cudaSuccess) return e;
   e = launch_next(k_diff_dkdv_tc<D>, dim3(g.ntile * g.Hk), kDiffThreads, smem, s, tk, tv, tq, tdo, g, L, b.tiles, b.seq,
-                  b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
+                  b.amax, b.rowx, b.tmax, b.lse, b.delta, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, c2, scale, err);
   if (e != cudaSuccess) return e;
   return launch_next(k_diff_dq_tc<D>, dim3(g.ntile * g.H), kDiffThreads, smem_q, s, tq, tdo, tk, tv, g, L, b.tiles, b.seq,
-                     b.amax, b.amax_do, b.lse, b.delta, (__nv_bfloat16*)dq, b.part, c2, scale, err);
+                     b.amax, b.rowx, b.lse, b.delta, (__nv_bfloat16*)dq, b.part, c2, scale, err);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_bwd_tc(const DiffGeom& g, const DiffTC& b, const void* dout, const void* lam, void* dq, void* dk,
                                void* dv, void* dlam, int* err, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(b.amax_do, 0, (size_t)g.B * g.Hk * sizeof(uint32_t), s);
-  if (e != cudaSuccess) return e;
-  e = g.D == 64 ? bwd_t<64>(g, b, dout, lam, dq, dk, dv, err, s) : bwd_t<128>(g, b, dout, lam, dq, dk, dv, err, s);
+  cudaError_t e = g.D == 64 ? bwd_t<64>(g, b, dout, lam, dq, dk, dv, err, s) : bwd_t<128>(g, b, dout, lam, dq, dk, dv, err, s);
   if (e != cudaSuccess) return e;
   return launch_diff_dlam(g.H, g.ntile, b.part, LH_BF16, dlam, s);
 }

@@ -654,7 +654,7 @@ namespace {
 struct DiffSizes {
   // parts of `saved`, and its size (seq .. vs: tensor cores)
   size_t tiles, seq, amax, qs, ks, vs, lse, om, saved;
-  size_t delta, part, amax_do, dos, ws;        // parts of the scratch, and its size
+  size_t delta, part, rowx, tmax, dos, ws;       // parts of the scratch, and its size
   int tc;
 };
 
@@ -714,7 +714,8 @@ lh_status make_diff(const lh_diff_config* c, DiffGeom* g, DiffSizes* z) {
     z->delta = part(2 * H * R * 4);
     z->part = part(H * (z->tc ? (size_t)g->ntile : (T + kDiffDeltaRows - 1) / kDiffDeltaRows) * 4);
     if (z->tc) {
-      z->amax_do = part((size_t)c->B * Hk * 4);
+      z->rowx = part(H * R * 4);
+      z->tmax = part(H * g->ntile * 4);
       z->dos = part(H * R * D * 2);
     }
     z->ws = at;
@@ -737,7 +738,8 @@ DiffTC diff_tc(const DiffSizes& z, void* saved, void* ws) {
   if (w) {
     b.delta = reinterpret_cast<float*>(w + z.delta);
     b.part = reinterpret_cast<float*>(w + z.part);
-    b.amax_do = reinterpret_cast<uint32_t*>(w + z.amax_do);
+    b.rowx = reinterpret_cast<int*>(w + z.rowx);
+    b.tmax = reinterpret_cast<int*>(w + z.tmax);
     b.dos = reinterpret_cast<__half*>(w + z.dos);
   }
   return b;
