@@ -498,11 +498,11 @@ lh_status lh_diff_plan(const lh_diff_config* cfg, lh_diff_plan_t* out);
  * read nor written, and a sequence's rows are read for that sequence alone.
  * packed = 0: cu is NULL. bf16 I/O runs on the tensor cores (fp16 operands
  * with a power of two per sequence and key/value head, as in lh_attn_fwd: a
- * value of q, k or v 2^-14 and less of the largest one may lose bits, down to
- * 2^-22 of it; a non-finite
- * value is reported, LH_ERR_DEVICE detail 102), fp32 in fp32 arithmetic. A
- * non-finite k or v value may reach every row of its sequence and head (0 times
- * it is not 0), no other. */
+ * value of q, k or v 2^-14 and less of the largest finite one may lose bits, down
+ * to 2^-22 of it; a non-finite value is reported, LH_ERR_DEVICE detail 102), fp32
+ * in fp32 arithmetic. A non-finite q value stays in its own row. A non-finite k or
+ * v value may reach every row of its sequence and head (0 times it is not 0), no
+ * other. */
 lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void* k, const void* v, const void* lam,
                            const int32_t* cu, void* o, void* saved, size_t saved_bytes, void* stream);
 
@@ -513,7 +513,8 @@ lh_status lh_diff_attn_fwd(const lh_diff_config* cfg, const void* q, const void*
  * bf16: every row of dout has a power of two of its own, so a dq row is as
  * accurate as its own size allows; what a query adds to a key's dk and dv is
  * rounded at 2^-38 and more below what the largest row that sees the key's tile
- * could add. */
+ * could add. A non-finite q or dout value reaches its own row of dq, and may reach
+ * every row of dk and dv of its sequence and key/value head. */
 lh_status lh_diff_attn_bwd(const lh_diff_config* cfg, const void* dout, const void* q, const void* k, const void* v,
                            const void* lam, const int32_t* cu, const void* saved, size_t saved_bytes,
                            void* ws, size_t ws_bytes, void* dq, void* dk, void* dv, void* dlam, void* stream);

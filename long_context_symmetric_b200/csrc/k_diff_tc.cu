@@ -52,6 +52,15 @@ constexpr float kPBias = 7.f;       // P is held at 2^7 times its value
 
 // ---------------------------------------------------------------- working copies
 
+// absmax8_bf16 of the finite ones: a value that is not finite says nothing about the
+// power that the others need.
+__device__ uint32_t absmax8_finite(const uint4& r) {
+  uint32_t m = 0;
+  for (const uint32_t w : {r.x, r.y, r.z, r.w})
+    for (const uint32_t x : {(w & 0x7FFFu) << 16, w & 0x7FFF0000u}) m = max(m, x < 0x7F800000u ? x : 0);
+  return m;
+}
+
 // One 128-row tile of one head of q, k or v. blockIdx.y: H query heads, then Hk
 // of k, Hk of v. REDO: only the heads whose power is not 2^0.
 template <bool REDO>
@@ -84,7 +93,14 @@ __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_
     const int r = i / nv, c = (i - r * nv) * 8;
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (r0 + r < t.y) raw = __ldg(reinterpret_cast<const uint4*>(src + (long long)(r0 + r) * ld + c));
-    if (!REDO) mx = max(mx, absmax8_bf16(raw));
+    if (!REDO) {
+      uint32_t m8 = absmax8_bf16(raw);
+      if (m8 >= 0x7F800000u) {
+        fin = false;
+        m8 = absmax8_finite(raw);
+      }
+      mx = max(mx, m8);
+    }
     uint4 out;
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
@@ -96,7 +112,6 @@ __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_
     *reinterpret_cast<uint4*>(dst + (size_t)r * g.D + c) = out;
   }
   if (!REDO) {
-    fin = mx < 0x7F800000u;
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if ((threadIdx.x & 31) == 0 && mx > *am) atomicMax(am, mx);

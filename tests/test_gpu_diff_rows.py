@@ -187,3 +187,37 @@ def test_packed_sequences_of_unlike_size():
             val, err = reference(*part, lam, do[lo:hi], OP["bf16"])
             for n in ("dq", "dk", "dv"):
                 assert_within(got[n][lo:hi], val[n], HALF["bf16"] * val[n].abs() + 1.01 * err[n], (n, lo))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("mul", [1.0, 2.0 ** 20, 2.0 ** -20])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_query_that_is_not_finite_stays_in_its_row(bad, mul, dtype):
+    """Whatever size the other queries have: their outputs and gradients keep their bits."""
+    T, H, Hk, D, row = 300, 4, 2, 64, 171
+    q, k, v, do = (rand(i, T, n, D, dtype=dtype) for i, n in enumerate((H, Hk, Hk, H)))
+    q, k, lam = q * mul, k / mul, torch.full((H,), 0.5, dtype=DT[dtype], device=DEV)
+    cfg = lh.make_diff_config(1, T, H, D, dtype, Hk)
+
+    def run(q, do):
+        ws = lh.DiffWorkspace(cfg, DEV)
+        o, dq, dk, dv, dlam = (torch.empty_like(t) for t in (q, q, k, v, lam))
+        lh.diff_attn_fwd(cfg, q, k, v, lam, o, ws)
+        lh.diff_attn_bwd(cfg, do, q, k, v, lam, ws, dq, dk, dv, dlam)
+        torch.cuda.synchronize()
+        return lh.get_device_error()[1], o, dq, dk, dv, dlam
+
+    code, *ref = run(q, do)
+    assert code == 0 and all(t.isfinite().all() for t in ref)
+    q2, do2 = q.clone(), do.clone()
+    q2[row, 1, 3] = do2[row, 1, 5] = bad
+    same = torch.ones(T, H, dtype=torch.bool, device=DEV)
+    same[row, 1] = False
+    for args in ((q2, do), (q, do2)):
+        code, o, dq, dk, dv, dlam = run(*args)
+        assert code in ((0,) if dtype == "fp32" else (101, 102))
+        assert torch.equal(o[same], ref[0][same]) and torch.equal(dq[same], ref[1][same])
+        assert not dq[~same].isfinite().all()
+        assert torch.equal(dk[:, 1], ref[2][:, 1]) and torch.equal(dv[:, 1], ref[3][:, 1])
+        keep = [0, 2, 3]
+        assert torch.equal(dlam[keep], ref[4][keep])
