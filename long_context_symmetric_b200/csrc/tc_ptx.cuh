@@ -91,26 +91,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// The same bounded wait for a warp whose wake-up is not urgent and that shares
-// its SM sub-partition with a compute warp: it sleeps between tries instead of
-// taking issue slots (in the differential attention's forward pass the softmax
-// warps next to the spinning issuer took 1,100 cycles for what took the others
-// 740).
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, volatile Abort* ab, int* err, int site) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
-    __nanosleep(40);
-    if (mbar_try_wait(bar, parity)) return true;
-    if (ab->flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      ab->flag = 1;
-      if (err && atomicCAS(err, 0, (int)LH_ERR_TIMEOUT) == 0) atomicExch(err + 1, site);
-      return false;
-    }
-  }
-}
-
 // 3-D tiled TMA load into shared memory, completion signalled on `bar`.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
                                             int c1, int c2) {
