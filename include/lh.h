@@ -434,7 +434,8 @@ lh_status lh_norm_bwd(const lh_norm_config* cfg, const void* dy, const void* x, 
 /* Rotary positions. Pair i of a row turns by pos[axis[i]] * freq[i] (radians):
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  * the elements behind the first `rot` are copied. Angles in 64 bits, rotation
- * in fp32, one rounding into dtype. */
+ * in fp32, one rounding into dtype. Rows that hold two maps (lh_diff_attn_fwd) are
+ * rotated map by map: as 2 H and 2 Hk heads of D/2 elements. */
 #define LH_ROPE_MAX_AXES 8
 #define LH_ROPE_MAX_D 1024
 typedef enum {
@@ -466,7 +467,8 @@ lh_status lh_rope(const lh_rope_config* cfg, const void* q, const void* k, const
                   const int32_t* axis, int inverse, void* qo, void* ko, void* stream);
 
 /* Causal differential attention: a head's q and k rows of D elements hold two
- * maps of D/2 (first half: map 1, second half: map 2),
+ * maps of D/2 (first half: map 1, second half: map 2; lh_rope takes them as 2 H
+ * heads of D/2, so that a score depends on the distance of its positions alone),
  *   o = A1 v - lam A2 v,  A_m = softmax(q_m k_m^T / sqrt(D/2) + causal mask).
  * Query head h reads key/value head h / (H / Hk). */
 typedef struct {

@@ -767,9 +767,19 @@ class Rotary(torch.autograd.Function):
         return gq, gk, None, None, None
 
 
-def rotary(q, k, pos, plan: RopePlan, pairs: str = "half"):
-    """q [B, N, H, D], k [B, N, Hk, D] rotated by positions pos (see RopePlan.positions)."""
-    return Rotary.apply(q, k, pos, plan, pairs)
+def rotary(q, k, pos, plan: RopePlan, pairs: str = "half", maps: int = 1):
+    """q [B, N, H, D], k [B, N, Hk, D] rotated by positions pos (see RopePlan.positions).
+
+    maps: a row holds that many maps of D/maps elements, each rotated by itself (plan.rot <= D/maps). In front of
+    differential_attention: 2. Rotated as a whole, a "half" pair would join an element of the first map with one of the
+    second, and a map's scores would depend on where its tokens stand, not on their distance alone."""
+    if maps == 1:
+        return Rotary.apply(q, k, pos, plan, pairs)
+    if maps < 1 or q.shape[-1] % maps or k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"rotary: {maps} maps in rows of {q.shape[-1]} (q) and {k.shape[-1]} (k) elements")
+    cut = lambda t: t.reshape(*t.shape[:-2], t.shape[-2] * maps, t.shape[-1] // maps)  # noqa: E731
+    qo, ko = Rotary.apply(cut(q), cut(k), pos, plan, pairs)
+    return qo.view(q.shape), ko.view(k.shape)
 
 
 class DifferentialAttention(torch.autograd.Function):
@@ -806,8 +816,8 @@ class DifferentialAttention(torch.autograd.Function):
 
 
 def differential_attention(q, k, v, lam, cu=None):
-    """o = (softmax map 1 - lam * softmax map 2) v, causal; q [B, N, H, D], k, v [B, N, Hk, D], lam [H]. With cu
-    (int32 [sequences + 1], device): q [T, H, D] and so on, the sequences packed one behind the other."""
+    """o = (softmax map 1 - lam * softmax map 2) v, causal; q [B, N, H, D], k, v [B, N, Hk, D], lam [H]. A head's q and k
+    rows hold map 1 in their first half and map 2 in the second (positions: rotary with maps=2). With cu (int32 [sequences + 1], device): q [T, H, D] and so on, the sequences packed one behind the other."""
     # without a backward pass to come nothing is kept for one
     train = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
     return DifferentialAttention.apply(q, k, v, lam, cu, train)

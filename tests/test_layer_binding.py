@@ -77,3 +77,13 @@ def test_a_bad_configuration_is_named_first(recorder):
     with pytest.raises(lh.LHError, match="status 2"):
         lh.norm_fwd(lh.make_norm_config(4, 64, eps=-1.0), x, None, None, x)
     assert recorder.launched == []
+
+
+def test_maps_have_to_fit_the_rows(recorder):
+    q, pos, plan = torch.zeros(1, 4, 2, 64, dtype=BF), torch.arange(4, dtype=torch.int32), lh.RopePlan(32, device="cpu")
+    for maps in (0, -1, 3):
+        with pytest.raises(ValueError, match="maps"):
+            lh.rotary(q, q, pos, plan, maps=maps)
+    with pytest.raises(lh.LHError, match="status 2"):       # tables of a whole row on half of one
+        lh.rotary(q, q, pos, lh.RopePlan(64, device="cpu"), maps=2)
+    assert recorder.launched == []
