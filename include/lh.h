@@ -483,6 +483,13 @@ typedef struct {
                                     o (and dout); 0: contiguous; multiples of 8, >= heads * D */
 } lh_diff_config;
 
+/* Sizes. A sequence takes whole tiles (128 rows; fp32: 64) and one more is set
+ * aside for each, in both buffers (bf16) and in blocks of the launches, and
+ * placing a tile looks at every sequence: many short sequences cost far more than
+ * their rows (bf16, training: 4,096 sequences in 8,192 rows of 8 heads of 64 save
+ * 2.8 GB and use 0.6 GB of scratch). bf16 keeps working copies of q, k, v in
+ * `saved` in any case (3 times o in all), training adds both maps' outputs (2
+ * times o) and statistics; fp32 keeps those two alone. */
 typedef struct {
   size_t saved_bytes;        /* written by lh_diff_attn_fwd, read by lh_diff_attn_bwd */
   size_t ws_bytes;           /* scratch of lh_diff_attn_bwd (0 unless train) */

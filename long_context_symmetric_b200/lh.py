@@ -419,6 +419,11 @@ def lighthouse_attention(q, k, v, p: int, L: int, K: int, accum: str = "fp"):
 # ---------------------------------------------------------------------------
 # operators of the layer around the attention: layer norm, rotary positions,
 # differential attention
+#
+# The functions can be captured into CUDA graphs, backward pass included, behind
+# one call outside of the capture. As with any torch operation no eager autograd
+# graph of the same leaves may live then (its gradient nodes belong to the stream
+# that it was made on, and torch would wait for that stream inside the capture).
 # ---------------------------------------------------------------------------
 
 _DTYPES = {"bf16": LH_BF16, "fp32": LH_FP32}
@@ -601,13 +606,15 @@ def diff_plan(cfg: DiffConfig) -> DiffPlan:
 
 
 class DiffWorkspace:
-    """Buffers of one differential attention: what the forward pass leaves for the backward, and the backward's
-    scratch. One forward + backward at a time: calls that overlap each need their own."""
+    """Buffers of one differential attention: what the forward pass leaves for the backward (saved: a forward pass's
+    buffer, otherwise a new one), and the backward's scratch (False: none). One forward + backward at a time: calls that
+    overlap each need their own."""
 
-    def __init__(self, cfg: DiffConfig, device):
+    def __init__(self, cfg: DiffConfig, device, saved=None, scratch: bool = True):
         self.plan = pl = diff_plan(cfg)
-        self.saved = torch.empty(max(pl.saved_bytes, 16), dtype=torch.uint8, device=device)
-        self.ws = torch.empty(max(pl.ws_bytes, 16), dtype=torch.uint8, device=device) if cfg.train else None
+        new = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=device)  # noqa: E731
+        self.saved = new(pl.saved_bytes) if saved is None else saved
+        self.ws = new(pl.ws_bytes) if cfg.train and scratch else None
 
 
 def _diff_check(f, dev, cfg, cu, lam, ws, rows):
@@ -797,21 +804,22 @@ class DifferentialAttention(torch.autograd.Function):
         name = type_name(q, "differential_attention")
         cfg = (make_diff_config(cu.numel() - 1, 0, H, D, name, Hk, rows=q.shape[0], train=train) if packed
                else make_diff_config(q.shape[0], q.shape[1], H, D, name, Hk, train=train))
-        ws = DiffWorkspace(cfg, q.device)
+        ws = DiffWorkspace(cfg, q.device, scratch=False)
         # packed: rows outside the sequences are not written by the kernels
         o = torch.zeros_like(q) if packed else torch.empty_like(q)
         diff_attn_fwd(cfg, q, k, v, lam, o, ws, cu=cu)
-        ctx.cfg, ctx.ws = cfg, ws
-        ctx.save_for_backward(q, k, v, lam, cu)
+        if train:
+            ctx.cfg = cfg
+            ctx.save_for_backward(q, k, v, lam, cu, ws.saved)
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do):
-        q, k, v, lam, cu = ctx.saved_tensors
+        q, k, v, lam, cu, saved = ctx.saved_tensors
         new = torch.zeros_like if ctx.cfg.packed else torch.empty_like
         dq, dk, dv, dlam = new(q), new(k), new(v), torch.empty_like(lam)
-        diff_attn_bwd(ctx.cfg, _whole(do), q, k, v, lam, ctx.ws, dq, dk, dv, dlam, cu=cu)
+        diff_attn_bwd(ctx.cfg, _whole(do), q, k, v, lam, DiffWorkspace(ctx.cfg, q.device, saved), dq, dk, dv, dlam, cu=cu)
         return dq, dk, dv, dlam, None, None
 
 
