@@ -13,6 +13,7 @@ that a kernel holds a value in:
 """
 
 import math
+import os
 
 import pytest
 import torch
@@ -22,6 +23,7 @@ from long_context_symmetric_b200 import lh
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
+SIMT = os.environ.get("LH_ATTN_SIMT", "").startswith("1")      # bf16 in fp32 arithmetic, which reports nothing
 OP = {"fp32": 0.0, "bf16": torch.finfo(torch.float16).eps / 2}
 
 
@@ -215,7 +217,7 @@ def test_a_query_that_is_not_finite_stays_in_its_row(bad, mul, dtype):
     same[row, 1] = False
     for args in ((q2, do), (q, do2)):
         code, o, dq, dk, dv, dlam = run(*args)
-        assert code in ((0,) if dtype == "fp32" else (101, 102))
+        assert code in ((0,) if dtype == "fp32" or SIMT else (101, 102))
         assert torch.equal(o[same], ref[0][same]) and torch.equal(dq[same], ref[1][same])
         assert not dq[~same].isfinite().all()
         assert torch.equal(dk[:, 1], ref[2][:, 1]) and torch.equal(dv[:, 1], ref[3][:, 1])
