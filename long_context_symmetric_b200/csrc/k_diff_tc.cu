@@ -93,14 +93,7 @@ __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_
     const int r = i / nv, c = (i - r * nv) * 8;
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (r0 + r < t.y) raw = __ldg(reinterpret_cast<const uint4*>(src + (long long)(r0 + r) * ld + c));
-    if (!REDO) {
-      uint32_t m8 = absmax8_bf16(raw);
-      if (m8 >= 0x7F800000u) {
-        fin = false;
-        m8 = absmax8_finite(raw);
-      }
-      mx = max(mx, m8);
-    }
+    if (!REDO) mx = max(mx, absmax8_bf16(raw));
     uint4 out;
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
     uint32_t* o = reinterpret_cast<uint32_t*>(&out);
@@ -112,6 +105,14 @@ __global__ void __launch_bounds__(256) k_diff_pack(const DiffGeom g, const __nv_
     *reinterpret_cast<uint4*>(dst + (size_t)r * g.D + c) = out;
   }
   if (!REDO) {
+    if (mx >= 0x7F800000u) {           // rare: the thread's values once more
+      fin = false;
+      mx = 0;
+      for (int i = threadIdx.x; i < kDiffTileTC * nv; i += 256) {
+        const int r = i / nv, c = (i - r * nv) * 8;
+        if (r0 + r < t.y) mx = max(mx, absmax8_finite(__ldg(reinterpret_cast<const uint4*>(src + (long long)(r0 + r) * ld + c))));
+      }
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if ((threadIdx.x & 31) == 0 && mx > *am) atomicMax(am, mx);
