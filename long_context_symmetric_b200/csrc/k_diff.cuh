@@ -49,8 +49,8 @@ using DiffTile = int4;
 
 // The block's place: tile and head. The tiles of `per` heads go together, the long
 // ones of all of them first, so that no long walk starts late (head by head, 16
-// heads of 8,192 tokens took 1,587 us forward and backward against 1,550, nine
-// documents of 7,001 tokens 421 against 372). As many heads as their streamed rows
+// heads of 8,192 tokens took 1,587 us forward and backward against 1,550, in loops
+// too short for the power cap, nine documents of 7,001 tokens 421 against 372). As many heads as their streamed rows
 // fit L2 together: beyond it they are read from HBM again and again (8 heads of
 // 65,536 tokens, all together: 2 % slower than one by one).
 __device__ __forceinline__ void diff_place(const DiffOrder& r, int block, int& rank, int& head) {

@@ -15,6 +15,10 @@
 // A first pass copies with the power 2^0 and records the magnitudes; a second
 // launch redoes the heads that need another power (others leave at once).
 //
+// For training both maps' outputs A_m v are kept in fp16, 11 bits where o has 8:
+// the backward forms d_m = <do, A_m v> of them, and a d_m off by 2^-12 of its terms
+// is below what the rounding of the gradients adds (fp32 would double what is kept).
+//
 // k_diff_fwd_tc. One CTA per 128-row query tile and head; both maps share the
 // rows, so the second stream of tiles that keeps the tensor core busy during a
 // softmax is the second map, and K and V tiles are loaded once for both.
@@ -32,7 +36,8 @@
 // Per 128 x 128 pair of tiles: 768 * 16,384 flops against 32,768 exponentials,
 // 1,536 tensor cycles against 2,048 of the special-function unit: it is the
 // exponentials that bound it. Measured at 16 heads of 8,192 tokens, D = 128: 397 us,
-// 1,037 TFLOP/s, and 10 us per CTA besides the pairs; 3,110 cycles per pair (score wait 1,100, loads and maximum 420,
+// 1,037 TFLOP/s (440 in a long loop under the power cap), and 10 us per CTA besides the
+// pairs; 3,110 cycles per pair (score wait 1,100, loads and maximum 420,
 // exponentials 1,400 per map, the two maps half a turn apart). Slower: keys in
 // halves of 64 with two score buffers per map (the N = 64 score products cost more
 // than the waits they hide), an issuer per map, a share of the exponentials as

@@ -46,7 +46,8 @@
 // run under the exponentials of tile t, dQ(t) and Y(t+1) under those of t+1.
 // 32,768 exponentials per pair in each kernel: 2,048 cycles of the special-
 // function unit against 2,048 (dk, dv) and 1,536 (dq) tensor cycles. Measured at 16
-// heads of 8,192 tokens, D = 128: 629 and 458 us, 5,100 and 3,300 cycles per pair:
+// heads of 8,192 tokens, D = 128: 630 and 458 us (696 and 512 in a long loop under the
+// power cap), 5,100 and 3,300 cycles per pair:
 // the two warpgroups exponentiate (1,050 cycles per map) and multiply (470 .. 700)
 // at the same time, so the two pipes take turns. Giving each warpgroup its own
 // 64-column halves, half a tile apart, was slower (1,000 and 800 us): score products

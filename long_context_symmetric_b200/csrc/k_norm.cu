@@ -24,9 +24,10 @@
 // form a row takes goes by its length, type and alignment, never by the number of
 // rows, so a row has the same bits in any batch. Arithmetic goes in packed pairs.
 //
-// Measured: 98,304 rows of 2,048 bf16 148 us forward (5.4 TB/s), 222 us backward
-// (5.4), 4 us the sums; 1,048,576 of 128 96 us (5.6) and 133 us (6.1); 5,003 of 1,537
-// fp32 19 and 33 us.
+// Measured: 98,304 rows of 2,048 bf16 149 us forward (5.4 TB/s), 222 us backward
+// (5.4), 4 us the sums, of fp32 296 (5.4) and 367 (6.6); 1,048,576 of 128 bf16 99 us
+// (5.4) and 134 us (6.0); 5,003 of 1,537 fp32 19 and 33 us. 8,192 of 16,384 bf16 125 us
+// forward (4.3), but 606 backward (1.3): the columns' sums in shared memory.
 //
 // Rows of odd length, or whose stride is no multiple of 8 elements, are read
 // element by element with the columns dealt out to neighbouring lanes (VEC =

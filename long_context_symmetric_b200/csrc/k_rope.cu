@@ -14,8 +14,9 @@
 // pair, shared by all heads) in shared memory while those are under way, then
 // rotate and store. W elements to a load: 16 bytes when the rows allow it, down
 // to single elements for row lengths, strides or rotated widths of odd size.
-// Measured: 524,288 tokens of 32 heads of 128 bf16 1.34 ms, 6.4 TB/s (a plain copy
-// on the same GPU: 6.5); 256 tokens 4.2 us.
+// Measured: 524,288 tokens of 32 heads of 128 bf16 1.34 - 1.48 ms from GPU to GPU, 5.8
+// - 6.4 TB/s (a plain copy: 6.5); 256 tokens 4.2 us; 2 x 8,191 tokens of 10 heads of 64,
+// 48 rotated, fp32 15 us (1,366 blocks on 444 places: the fourth wave runs nearly empty).
 #include "lh_common.cuh"
 
 namespace lh {
