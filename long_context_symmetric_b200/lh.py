@@ -165,13 +165,20 @@ def _check(status: int, name: str):
         raise LHError(status, name)
 
 
-def _p(t):
+def _ptr(t):
     """Data pointer of a tensor (or None / int passthrough)."""
     if t is None:
         return None
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _p(t):
+    """The same of a tensor on a CUDA device: host memory never reaches a kernel."""
+    if isinstance(t, torch.Tensor) and not t.is_cuda:
+        raise ValueError(f"a tensor is on {t.device}, a CUDA device is wanted")
+    return _ptr(t)
 
 
 def _stream(stream):
@@ -541,7 +548,7 @@ def norm_fwd(cfg, x, w, b, y, mean=None, rstd=None, stream=None):
     _need(f, dev, "b", b, wt, d)
     _need(f, dev, "mean", mean, torch.float32, M)
     _need(f, dev, "rstd", rstd, torch.float32, M)
-    _call(f, dev, stream, ctypes.byref(cfg), _p(x), _p(w), _p(b), _p(y), _p(mean), _p(rstd))
+    _call(f, dev, stream, ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mean), _ptr(rstd))
 
 
 def norm_bwd(cfg, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
@@ -555,7 +562,7 @@ def norm_bwd(cfg, dy, x, w, mean, rstd, dx, dw, db, ws, stream=None):
     _need(f, dev, "dw", dw, wt, d)
     _need(f, dev, "db", db, wt, d)
     _need(f, dev, "ws", ws, torch.uint8, 0)
-    _call(f, dev, stream, ctypes.byref(cfg), _p(dy), _p(x), _p(w), _p(mean), _p(rstd), _p(dx), _p(dw), _p(db), _p(ws),
+    _call(f, dev, stream, ctypes.byref(cfg), _ptr(dy), _ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws),
           ws.numel() if ws is not None else 0)
 
 
@@ -589,7 +596,7 @@ def rope(cfg, q, k, pos, freq, axis, qo, ko, inverse=False, stream=None):
             _rows_fit(f, dev, "pos", pos, torch.int64 if cfg.pos64 else torch.int32, cfg.axes, cfg.pos_as, N)
     _need(f, dev, "freq", freq, torch.float64, R)
     _need(f, dev, "axis", axis, torch.int32, R)
-    _call(f, dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(pos), _p(freq), _p(axis), int(inverse), _p(qo), _p(ko))
+    _call(f, dev, stream, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(pos), _ptr(freq), _ptr(axis), int(inverse), _ptr(qo), _ptr(ko))
 
 
 def make_diff_config(B, N, H, D, dtype="bf16", Hk=None, rows=None, train=True, ldq=0, ldk=0, ldv=0, ldo=0) -> DiffConfig:
@@ -633,7 +640,7 @@ def diff_attn_fwd(cfg, q, k, v, lam, o, ws: DiffWorkspace, cu=None, stream=None)
     f, dev = "lh_diff_attn_fwd", q.device
     _diff_check(f, dev, cfg, cu, lam, ws, (("q", q, cfg.ldq, cfg.H), ("k", k, cfg.ldk, cfg.Hk),
                                            ("v", v, cfg.ldv, cfg.Hk), ("o", o, cfg.ldo, cfg.H)))
-    _call(f, dev, stream, ctypes.byref(cfg), _p(q), _p(k), _p(v), _p(lam), _p(cu), _p(o), _p(ws.saved), ws.saved.numel())
+    _call(f, dev, stream, ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(cu), _ptr(o), _ptr(ws.saved), ws.saved.numel())
 
 
 def diff_attn_bwd(cfg, dout, q, k, v, lam, ws: DiffWorkspace, dq, dk, dv, dlam, cu=None, stream=None):
@@ -643,8 +650,8 @@ def diff_attn_bwd(cfg, dout, q, k, v, lam, ws: DiffWorkspace, dq, dk, dv, dlam, 
                  ("k", k, cfg.ldk, cfg.Hk), ("dk", dk, cfg.ldk, cfg.Hk), ("v", v, cfg.ldv, cfg.Hk), ("dv", dv, cfg.ldv, cfg.Hk)))
     _need(f, dev, "dlam", dlam, _TORCH[cfg.dtype], cfg.H)
     _need(f, dev, "ws", ws.ws, torch.uint8, 0)
-    _call(f, dev, stream, ctypes.byref(cfg), _p(dout), _p(q), _p(k), _p(v), _p(lam), _p(cu), _p(ws.saved),
-          ws.saved.numel(), _p(ws.ws), ws.ws.numel() if ws.ws is not None else 0, _p(dq), _p(dk), _p(dv), _p(dlam))
+    _call(f, dev, stream, ctypes.byref(cfg), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(cu), _ptr(ws.saved),
+          ws.saved.numel(), _ptr(ws.ws), ws.ws.numel() if ws.ws is not None else 0, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlam))
 
 
 def type_name(t, what):
@@ -825,7 +832,8 @@ class DifferentialAttention(torch.autograd.Function):
 
 def differential_attention(q, k, v, lam, cu=None):
     """o = (softmax map 1 - lam * softmax map 2) v, causal; q [B, N, H, D], k, v [B, N, Hk, D], lam [H]. A head's q and k
-    rows hold map 1 in their first half and map 2 in the second (positions: rotary with maps=2). With cu (int32 [sequences + 1], device): q [T, H, D] and so on, the sequences packed one behind the other."""
+    rows hold map 1 in their first half and map 2 in the second (positions: rotary with maps=2). With cu (int32
+    [sequences + 1], device): q [T, H, D] and so on, the sequences packed one behind the other."""
     # without a backward pass to come nothing is kept for one
     train = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
     return DifferentialAttention.apply(q, k, v, lam, cu, train)

@@ -1,4 +1,4 @@
-"""The binding of the layer operators against a stand-in for the library: what it passes on, and what it never does."""
+"""The binding against a stand-in for the library: what it passes on, and what it never does."""
 
 import pytest
 import torch
@@ -86,4 +86,17 @@ def test_maps_have_to_fit_the_rows(recorder):
             lh.rotary(q, q, pos, plan, maps=maps)
     with pytest.raises(lh.LHError, match="status 2"):       # tables of a whole row on half of one
         lh.rotary(q, q, pos, lh.RopePlan(64, device="cpu"), maps=2)
+    assert recorder.launched == []
+
+
+def test_the_path_refuses_host_memory_too(recorder):
+    t, f = torch.zeros(1, 256, 2, 64, dtype=BF), torch.zeros(1024)
+    cfg = lh.make_config(1, 2, 256, 64, 4, 2, 16)
+    for call in (lambda: lh.lighthouse_attention(t, t, t, 4, 2, 16), lambda: lh.Workspace(cfg, "cpu"),
+                 lambda: lh.pool(cfg, t, t, t, t, t, t, f.double(), f.int()), lambda: lh.gather(cfg, t, t, t, t, t, t, f.int(), f, t, t, t),
+                 lambda: lh.attn_fwd(cfg, t, t, t, f, f, f), lambda: lh.scatter_range(cfg, 0, 16, f, f.int(), t),
+                 lambda: lh.cp_pool(cfg, 2, 0, t, t, t, t, t, t, f.double(), f.int()),
+                 lambda: lh.selftest_exp2(f, f, f), lambda: lh.selftest_timeout(1000, f.int())):
+        with pytest.raises(ValueError, match="on cpu"):
+            call()
     assert recorder.launched == []
